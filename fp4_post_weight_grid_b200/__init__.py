@@ -34,7 +34,10 @@ __all__ = [
     "fp4q_nvfp4_gptq", "fp4q_gptq_workspace_bytes", "nvfp4_gptq", "fp4q_probe_wait", "fp4q_probe_copy",
     "quantize_batch", "fp4q_mxfp4_quant_group", "fp4q_nvfp4_sweep_group", "GROUP_MAX",
     "NVFP4Result", "MXFP4Result", "nvfp4_quantize", "mxfp4_quantize", "quantize_dual", "dequantize",
-    "FLAG_NONFINITE", "FLAG_RANGE", "FLAG_TIMEOUT",
+    "fp4q_linear", "fp4q_linear_group", "fp4q_matmul", "fp4q_matmul_group", "Epilogue", "ProductResult",
+    "linear", "linear_group", "matmul", "matmul_group",
+    "ACT_NONE", "ACT_RELU", "ACT_GELU", "ACT_GELU_TANH", "ACT_SILU",
+    "FLAG_NONFINITE", "FLAG_RANGE", "FLAG_TIMEOUT", "FLAG_OFFSETS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -45,7 +48,8 @@ _lib_lock = threading.Lock()
 OK, ERR_NULL, ERR_SHAPE, ERR_DTYPE, ERR_ALIGN, ERR_NONFINITE, ERR_CUDA, ERR_RANGE, ERR_ARG = range(9)
 F32, BF16 = 0, 1
 NVFP4, MXFP4 = 0, 1
-FLAG_NONFINITE, FLAG_RANGE, FLAG_TIMEOUT = 1, 2, 4
+FLAG_NONFINITE, FLAG_RANGE, FLAG_TIMEOUT, FLAG_OFFSETS = 1, 2, 4, 8
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
 BATCH_MAX = 128
 GROUP_MAX = 32
 NVFP4_BLOCK, MXFP4_BLOCK = 16, 32
@@ -56,7 +60,8 @@ EXPORTS = ("fp4q_version", "fp4q_status_string", "fp4q_last_cuda_error", "fp4q_g
            "fp4q_probe_e2m1", "fp4q_probe_e4m3", "fp4q_nvfp4_sweep_dynamic", "fp4q_dynamic_workspace_bytes",
            "fp4q_mma_scale_bytes", "fp4q_scales_to_mma_layout", "fp4q_focus_quant", "fp4q_mxfp4_unrotate",
            "fp4q_nvfp4_gptq", "fp4q_gptq_workspace_bytes", "fp4q_probe_wait",
-           "fp4q_probe_copy", "fp4q_mxfp4_quant_group", "fp4q_nvfp4_sweep_group")
+           "fp4q_probe_copy", "fp4q_mxfp4_quant_group", "fp4q_nvfp4_sweep_group",
+           "fp4q_linear", "fp4q_linear_group", "fp4q_matmul", "fp4q_matmul_group")
 
 
 class BatchTensor(ctypes.Structure):
@@ -68,6 +73,12 @@ class BatchTensor(ctypes.Structure):
                 ("nv_deq", ctypes.c_void_p), ("nv_loss", ctypes.c_void_p),
                 ("mx_codes", ctypes.c_void_p), ("mx_scales", ctypes.c_void_p),
                 ("mx_deq", ctypes.c_void_p), ("mx_loss", ctypes.c_void_p)]
+
+
+class Epilogue(ctypes.Structure):
+    """Mirror of fp4q_epilogue (include/fp4q.h)."""
+    _fields_ = [("bias", ctypes.c_void_p), ("mul", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("act", ctypes.c_int)]
 
 
 class Fp4qError(RuntimeError):
@@ -129,6 +140,11 @@ def _load_locked():
     sigs["fp4q_mxfp4_unrotate"] = [P, I, I64, I64, P, P, P]
     sigs["fp4q_nvfp4_gptq"] = [P, I64, I64, P, P, P, P, P, P, P, ctypes.c_size_t, P, P]
     sigs["fp4q_nvfp4_sweep_dynamic"] = [P, I, I64, I64, P, P, P, P, P, P, P, P, ctypes.c_size_t, P, P]
+    E, I32 = ctypes.POINTER(Epilogue), ctypes.c_int32
+    sigs["fp4q_linear"] = [I, P, I64, P, P, P, I64, I64, E, P, I, P, P]
+    sigs["fp4q_linear_group"] = [I, P, I64, P, I32, P, P, P, I64, I64, E, P, I, P, P]
+    sigs["fp4q_matmul"] = [I, P, P, P, I64, P, P, P, I64, I64, E, P, I, P, P]
+    sigs["fp4q_matmul_group"] = [I, P, P, P, I64, P, I32, P, P, P, I64, I64, E, P, I, P, P]
     for name, args in sigs.items():
         fn = getattr(lib, name)
         fn.restype = I
@@ -365,7 +381,14 @@ def fp4q_scales_to_mma_layout(scales: torch.Tensor, out: torch.Tensor, stream=No
 
 
 def mma_scales(scales: torch.Tensor, stream=None) -> torch.Tensor:
-    """Allocating form of fp4q_scales_to_mma_layout (flat uint8 tensor)."""
+    """Allocating form of fp4q_scales_to_mma_layout (flat uint8 tensor).  A 3-D
+    [groups][rows][scale_cols] tensor gives [groups][bytes], one layout per group."""
+    if scales.dim() == 3:
+        groups, rows, scols = scales.shape
+        out = torch.empty((groups, fp4q_mma_scale_bytes(rows, scols)), dtype=torch.uint8, device=scales.device)
+        for g in range(groups):
+            fp4q_scales_to_mma_layout(scales[g], out[g], stream)
+        return out
     rows, scols = scales.shape
     out = torch.empty(fp4q_mma_scale_bytes(rows, scols), dtype=torch.uint8, device=scales.device)
     fp4q_scales_to_mma_layout(scales, out, stream)
@@ -539,6 +562,84 @@ def fp4q_dequant(fmt: int, codes, scales, d_global_scale, rows: int, cols: int, 
     op = _dev(out, "out", None, n, dev)
     _check(load().fp4q_dequant(int(fmt), cp, sp, gp, rows, cols, op, _wdtype(out), _stream(stream)),
            "fp4q_dequant")
+
+
+def _product(name, fmt, x, x_scales, x_global_scale, offsets, w_codes, w_scales, w_global_scale, y, d_status, bias,
+             act, mul, residual, stream):
+    """Checks and marshalling of the four products.  x_scales None: x is bf16;
+    offsets None: one weight."""
+    if fmt not in (NVFP4, MXFP4):
+        raise Fp4qError(ERR_DTYPE, name)
+    block = MXFP4_BLOCK if fmt == MXFP4 else NVFP4_BLOCK
+    dev, packed, grouped = y.device, x_scales is not None, offsets is not None
+    if x.dim() != 2 or y.dim() != 2 or w_codes.dim() != (3 if grouped else 2):
+        raise ValueError(f"{name}: x and y are 2-D, w_codes {'[groups, n, k/2]' if grouped else '[n, k/2]'}")
+    groups = w_codes.shape[0] if grouped else 1
+    n, k, m = w_codes.shape[-2], 2 * w_codes.shape[-1], x.shape[0]
+    if x.shape[1] != (k // 2 if packed else k) or y.shape[0] != m or y.shape[1] != n:
+        raise ValueError(f"{name}: x {tuple(x.shape)}, w_codes {tuple(w_codes.shape)} and y {tuple(y.shape)} do not fit")
+    if k == 0 or k % 32:
+        raise Fp4qError(ERR_SHAPE, f"{name}: k = {k} is not a positive multiple of 32")
+    lib = load()
+    nv, dt = fmt == NVFP4, y.dtype
+    if nv and (w_global_scale is None or (packed and x_global_scale is None)):
+        raise Fp4qError(ERR_NULL, f"{name}: NVFP4 needs its global scales")
+    ep = Epilogue(_dev(bias, "bias", dt, groups * n, dev), _dev(mul, "mul", dt, m * n, dev),
+                  _dev(residual, "residual", dt, m * n, dev), int(act))
+    args = [int(fmt), _dev(x, "x", torch.uint8 if packed else torch.bfloat16, None, dev)]
+    if packed:
+        args += [_dev(x_scales, "x_scales", torch.uint8, m * (k // block), dev),
+                 _dev(x_global_scale, "x_global_scale", torch.float32, 1, dev) if nv else None]
+    args.append(m)
+    if grouped:
+        args += [_dev(offsets, "offsets", torch.int32, groups + 1, dev), groups]
+    args += [_dev(w_codes, "w_codes", torch.uint8, None, dev),
+             _dev(w_scales, "w_scales", torch.uint8, groups * int(lib.fp4q_mma_scale_bytes(n, k // block)), dev),
+             _dev(w_global_scale, "w_global_scale", torch.float32, groups, dev) if nv else None,
+             n, k, ctypes.byref(ep), _dev(y, "y", None, None, dev), _wdtype(y),
+             _dev(d_status, "d_status", torch.int32, 1, dev)]
+    with torch.cuda.device(dev):
+        _check(getattr(lib, name)(*args, _stream(stream)), name)
+
+
+def fp4q_linear(fmt: int, x, w_codes, w_scales, w_global_scale, y, d_status, bias=None, act: int = ACT_NONE, mul=None,
+                residual=None, stream=None) -> None:
+    """y = act(x W^T + bias) * mul + residual: bf16 `x` [m, k] times an FP4 weight
+    (`w_codes` [n, k/2], `w_scales` in the tiled layout of mma_scales, NVFP4
+    `w_global_scale`).  bias [n], mul and residual [m, n] have y's dtype (bf16
+    or float32); mul or residual may be y itself."""
+    _product("fp4q_linear", fmt, x, None, None, None, w_codes, w_scales, w_global_scale, y, d_status, bias, act, mul,
+             residual, stream)
+
+
+def fp4q_linear_group(fmt: int, x, offsets, w_codes, w_scales, w_global_scale, y, d_status, bias=None,
+                      act: int = ACT_NONE, mul=None, residual=None, stream=None) -> None:
+    """fp4q_linear per group (expert): rows offsets[g] .. offsets[g+1]-1 of x use
+    weight g.  `offsets` int32 [groups + 1] on the device, `w_codes` [groups, n,
+    k/2], `w_scales` the groups' tiled scales one after the other, bias [groups,
+    n].  Rows outside the offsets are left as they are."""
+    _product("fp4q_linear_group", fmt, x, None, None, offsets, w_codes, w_scales, w_global_scale, y, d_status, bias,
+             act, mul, residual, stream)
+
+
+def fp4q_matmul(fmt: int, x_codes, x_scales, x_global_scale, w_codes, w_scales, w_global_scale, y, d_status, bias=None,
+                act: int = ACT_NONE, mul=None, residual=None, stream=None) -> None:
+    """fp4q_linear with `x` in the weight's FP4 format: codes [m, k/2] and row-major
+    block scales [m, k/block] as the quantizers write them (NVFP4: and its global
+    scale)."""
+    if x_scales is None:
+        raise TypeError("fp4q_matmul: x_scales is missing")
+    _product("fp4q_matmul", fmt, x_codes, x_scales, x_global_scale, None, w_codes, w_scales, w_global_scale, y,
+             d_status, bias, act, mul, residual, stream)
+
+
+def fp4q_matmul_group(fmt: int, x_codes, x_scales, x_global_scale, offsets, w_codes, w_scales, w_global_scale, y,
+                      d_status, bias=None, act: int = ACT_NONE, mul=None, residual=None, stream=None) -> None:
+    """fp4q_matmul per group (expert), grouped as in fp4q_linear_group."""
+    if x_scales is None:
+        raise TypeError("fp4q_matmul_group: x_scales is missing")
+    _product("fp4q_matmul_group", fmt, x_codes, x_scales, x_global_scale, offsets, w_codes, w_scales, w_global_scale,
+             y, d_status, bias, act, mul, residual, stream)
 
 
 def fp4q_probe_e2m1(r: torch.Tensor, out: torch.Tensor, stream=None) -> None:
@@ -768,6 +869,52 @@ def dequantize(fmt: int, codes: torch.Tensor, scales: torch.Tensor, global_scale
     return out
 
 
+class ProductResult(NamedTuple):
+    y: torch.Tensor               # [m, n], out_dtype
+    status: torch.Tensor          # int32 [1], FLAG_* bits
+
+
+def _product_result(x, n, out_dtype):
+    return ProductResult(torch.empty((x.shape[0], n), dtype=out_dtype, device=x.device),
+                         torch.zeros(1, dtype=torch.int32, device=x.device))
+
+
+def linear(fmt: int, x, w_codes, w_scales, w_global_scale=None, bias=None, act: int = ACT_NONE, mul=None,
+           residual=None, out_dtype=torch.bfloat16, stream=None) -> ProductResult:
+    """Allocating form of fp4q_linear."""
+    r = _product_result(x, w_codes.shape[-2], out_dtype)
+    fp4q_linear(fmt, x, w_codes, w_scales, w_global_scale, r.y, r.status, bias, act, mul, residual, stream)
+    return r
+
+
+def linear_group(fmt: int, x, offsets, w_codes, w_scales, w_global_scale=None, bias=None, act: int = ACT_NONE,
+                 mul=None, residual=None, out_dtype=torch.bfloat16, stream=None) -> ProductResult:
+    """Allocating form of fp4q_linear_group (rows outside the offsets are undefined)."""
+    r = _product_result(x, w_codes.shape[-2], out_dtype)
+    fp4q_linear_group(fmt, x, offsets, w_codes, w_scales, w_global_scale, r.y, r.status, bias, act, mul, residual,
+                      stream)
+    return r
+
+
+def matmul(fmt: int, x_codes, x_scales, x_global_scale, w_codes, w_scales, w_global_scale=None, bias=None,
+           act: int = ACT_NONE, mul=None, residual=None, out_dtype=torch.bfloat16, stream=None) -> ProductResult:
+    """Allocating form of fp4q_matmul."""
+    r = _product_result(x_codes, w_codes.shape[-2], out_dtype)
+    fp4q_matmul(fmt, x_codes, x_scales, x_global_scale, w_codes, w_scales, w_global_scale, r.y, r.status, bias, act,
+                mul, residual, stream)
+    return r
+
+
+def matmul_group(fmt: int, x_codes, x_scales, x_global_scale, offsets, w_codes, w_scales, w_global_scale=None,
+                 bias=None, act: int = ACT_NONE, mul=None, residual=None, out_dtype=torch.bfloat16,
+                 stream=None) -> ProductResult:
+    """Allocating form of fp4q_matmul_group (rows outside the offsets are undefined)."""
+    r = _product_result(x_codes, w_codes.shape[-2], out_dtype)
+    fp4q_matmul_group(fmt, x_codes, x_scales, x_global_scale, offsets, w_codes, w_scales, w_global_scale, r.y,
+                      r.status, bias, act, mul, residual, stream)
+    return r
+
+
 def check_status(status: torch.Tensor) -> int:
     """Synchronize on the status word and raise on a device-reported flag."""
     v = int(status.item())
@@ -775,4 +922,6 @@ def check_status(status: torch.Tensor) -> int:
         raise Fp4qError(ERR_NONFINITE, "device status")
     if v & FLAG_RANGE:
         raise Fp4qError(ERR_RANGE, "device status")
+    if v & FLAG_OFFSETS:
+        raise Fp4qError(ERR_ARG, "device status: group offsets out of order or range")
     return v

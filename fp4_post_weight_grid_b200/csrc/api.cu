@@ -13,6 +13,7 @@
 #include "batch.h"
 #include "fp4q.h"
 #include "launch.h"
+#include "product.h"
 
 namespace fp4q {
 
@@ -572,6 +573,104 @@ fp4q_status fp4q_dequant(fp4q_format format, const uint8_t* codes, const uint8_t
     fp4q::launch_dequant(mx, codes, scales, d_global_scale, rows, cols, out, out_dt == FP4Q_BF16,
                          reinterpret_cast<cudaStream_t>(stream));
     return after_launch();
+}
+
+namespace {
+
+// The checks that the four products share, then the launch.  groups < 0: a
+// dense call (one weight, no offsets).
+fp4q_status product_call(fp4q::Product p, fp4q_format fmt, const fp4q_epilogue* ep, int32_t groups, fp4q_dtype out_dt,
+                         fp4q_stream_t stream)
+{
+    if ((fmt != FP4Q_NVFP4 && fmt != FP4Q_MXFP4) || !valid_dtype(out_dt)) return FP4Q_ERR_DTYPE;
+    const bool grouped = groups >= 0;
+    p.mx = fmt == FP4Q_MXFP4;
+    p.groups = grouped ? groups : 1;
+    p.out_bf16 = out_dt == FP4Q_BF16;
+    p.ep = ep ? *ep : fp4q_epilogue{nullptr, nullptr, nullptr, FP4Q_ACT_NONE};
+    if (p.ep.act < FP4Q_ACT_NONE || p.ep.act > FP4Q_ACT_SILU || p.groups > FP4Q_PRODUCT_GROUPS_MAX) return FP4Q_ERR_ARG;
+    // Rows and columns are 32-bit coordinates of the tensor copies, with room
+    // for a tile past the end.
+    constexpr int64_t kMost = INT32_MAX - 256;
+    if (p.m < 0 || p.n < 0 || p.k <= 0 || p.k % 32 != 0 || p.m > kMost || p.n > kMost || p.k > kMost ||
+        p.n * p.groups > kMost || !shape_ok(p.m, p.k, 1) || !shape_ok(p.n * p.groups, p.k, 1) || !shape_ok(p.m, p.n, 1))
+        return FP4Q_ERR_SHAPE;
+    if (p.m == 0 || p.n == 0 || p.groups == 0) return FP4Q_OK;
+    if (!p.x || !p.w || !p.w_scales || !p.y || !p.status || (grouped && !p.offsets) || (!p.mx && !p.w_S) ||
+        (p.packed && (!p.x_scales || (!p.mx && !p.x_S))))
+        return FP4Q_ERR_NULL;
+    if (!aligned(p.x, 16) || !aligned(p.w, 16) || !aligned(p.w_scales, 16) || !aligned(p.y, 16) ||
+        !aligned(p.status, 4) || (grouped && !aligned(p.offsets, 4)) || (!p.mx && !aligned(p.w_S, 4)) ||
+        (p.packed && (!aligned(p.x_scales, 4) || (!p.mx && !aligned(p.x_S, 4)))) || !aligned(p.ep.bias, 16) ||
+        !aligned(p.ep.mul, 16) || !aligned(p.ep.residual, 16))
+        return FP4Q_ERR_ALIGN;
+    p.w_scale_stride = fp4q::mma_scale_bytes(p.n, p.k / (p.mx ? FP4Q_MXFP4_BLOCK : FP4Q_NVFP4_BLOCK));
+    const cudaError_t e = fp4q::launch_product(p, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FP4Q_OK : cuda_failure(e);
+}
+
+fp4q::Product product_of(const void* x, int64_t m, const uint8_t* w_codes, const uint8_t* w_scales,
+                         const float* w_global_scale, int64_t n, int64_t k, void* y, int32_t* d_status)
+{
+    fp4q::Product p{};
+    p.x = x;
+    p.m = m;
+    p.w = w_codes;
+    p.w_scales = w_scales;
+    p.w_S = w_global_scale;
+    p.n = n;
+    p.k = k;
+    p.y = y;
+    p.status = d_status;
+    return p;
+}
+
+}  // namespace
+
+fp4q_status fp4q_linear(fp4q_format fmt, const void* x, int64_t m, const uint8_t* w_codes, const uint8_t* w_scales,
+                        const float* w_global_scale, int64_t n, int64_t k, const fp4q_epilogue* ep, void* y,
+                        fp4q_dtype out_dt, int32_t* d_status, fp4q_stream_t stream)
+{
+    return product_call(product_of(x, m, w_codes, w_scales, w_global_scale, n, k, y, d_status), fmt, ep, -1, out_dt,
+                        stream);
+}
+
+fp4q_status fp4q_linear_group(fp4q_format fmt, const void* x, int64_t m, const int32_t* offsets, int32_t groups,
+                              const uint8_t* w_codes, const uint8_t* w_scales, const float* w_global_scale, int64_t n,
+                              int64_t k, const fp4q_epilogue* ep, void* y, fp4q_dtype out_dt, int32_t* d_status,
+                              fp4q_stream_t stream)
+{
+    if (groups < 0) return FP4Q_ERR_SHAPE;
+    fp4q::Product p = product_of(x, m, w_codes, w_scales, w_global_scale, n, k, y, d_status);
+    p.offsets = offsets;
+    return product_call(p, fmt, ep, groups, out_dt, stream);
+}
+
+fp4q_status fp4q_matmul(fp4q_format fmt, const uint8_t* x_codes, const uint8_t* x_scales, const float* x_global_scale,
+                        int64_t m, const uint8_t* w_codes, const uint8_t* w_scales, const float* w_global_scale,
+                        int64_t n, int64_t k, const fp4q_epilogue* ep, void* y, fp4q_dtype out_dt, int32_t* d_status,
+                        fp4q_stream_t stream)
+{
+    fp4q::Product p = product_of(x_codes, m, w_codes, w_scales, w_global_scale, n, k, y, d_status);
+    p.packed = true;
+    p.x_scales = x_scales;
+    p.x_S = x_global_scale;
+    return product_call(p, fmt, ep, -1, out_dt, stream);
+}
+
+fp4q_status fp4q_matmul_group(fp4q_format fmt, const uint8_t* x_codes, const uint8_t* x_scales,
+                              const float* x_global_scale, int64_t m, const int32_t* offsets, int32_t groups,
+                              const uint8_t* w_codes, const uint8_t* w_scales, const float* w_global_scale, int64_t n,
+                              int64_t k, const fp4q_epilogue* ep, void* y, fp4q_dtype out_dt, int32_t* d_status,
+                              fp4q_stream_t stream)
+{
+    if (groups < 0) return FP4Q_ERR_SHAPE;
+    fp4q::Product p = product_of(x_codes, m, w_codes, w_scales, w_global_scale, n, k, y, d_status);
+    p.packed = true;
+    p.x_scales = x_scales;
+    p.x_S = x_global_scale;
+    p.offsets = offsets;
+    return product_call(p, fmt, ep, groups, out_dt, stream);
 }
 
 fp4q_status fp4q_probe_e2m1(const float* r, uint8_t* out, int64_t n, fp4q_stream_t stream)

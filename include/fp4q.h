@@ -546,6 +546,105 @@ fp4q_status fp4q_dequant(fp4q_format format, const uint8_t* codes, const uint8_t
                          fp4q_dtype out_dt, fp4q_stream_t stream);
 
 /*
+ * Products on FP4 weights
+ * -----------------------
+ * The quantizers above write a weight W[n][k] as codes and block scales; the
+ * four calls below multiply by it (the MR-GPTQ summary, technical sec. 3, runs
+ * the quantized weights through FP4 GEMM kernels on Blackwell; the pages give
+ * no interface for them).  With W[j][i] = E2M1(code) * s, s the element's block
+ * scale (E4M3 pattern or 2^(b-127)),
+ *   acc  = sum_i x[r][i] * W[j][i]        accumulated in binary32
+ *   z    = act(acc * S + bias[j])         S: the global scale(s), 1 for MXFP4
+ *   y[r][j] = z * mul[r][j] + residual[r][j]
+ * in binary32, rounded once to the output dtype; bias, mul and residual are
+ * left out where their pointer is NULL.  With mul the call is the second half
+ * of a gated layer (act(gate) * up).
+ *
+ * fp4q_linear, fp4q_linear_group   x is bf16: q * s has at most 6 significant
+ *     bits, so the decoded weight enters a bf16 product without any rounding.
+ * fp4q_matmul, fp4q_matmul_group   x is FP4 in the weight's format, as
+ *     fp4q_nvfp4_sweep_dynamic, fp4q_mxfp4_quant or (for weights quantized
+ *     with the same sign masks) fp4q_mxfp4_quant_hadamard write it.
+ * The group calls multiply the rows of each group (expert) by that group's
+ * own weight: rows offsets[g] .. offsets[g+1]-1 of x, mul, residual and y
+ * belong to group g, groups may be empty, and rows before offsets[0] or from
+ * offsets[groups] on are neither read nor written.
+ *
+ * Arguments (all four):
+ *   fmt         FP4Q_NVFP4 or FP4Q_MXFP4.
+ *   m, n, k     rows of x and y, rows of W, columns of both.  k is a positive
+ *               multiple of 32 (both formats); m and n are arbitrary.
+ *   x           bf16 [m][k], 16-byte aligned; or
+ *   x_codes     [m][k/2] bytes, 16-byte aligned, and
+ *   x_scales    [m][k/block] bytes, row-major, 4-byte aligned, and
+ *   x_global_scale  device float (NVFP4; ignored and may be NULL for MXFP4).
+ *   w_codes     [groups][n][k/2] bytes, 16-byte aligned.
+ *   w_scales    the block scales of each weight in the tiled layout of
+ *               fp4q_scales_to_mma_layout, 16-byte aligned; the groups'
+ *               fp4q_mma_scale_bytes(n, k/block) bytes one after the other.
+ *   w_global_scale  [groups] device floats (NVFP4; ignored and may be NULL
+ *               for MXFP4).
+ *   offsets     [groups + 1] device int32, non-decreasing, within [0, m].
+ *   groups      at most FP4Q_PRODUCT_GROUPS_MAX.
+ *   ep          HOST struct read during the call, or NULL for none of it:
+ *               bias [n] ([groups][n]), mul and residual [m][n], all of the
+ *               output dtype and 16-byte aligned.
+ *   y           [m][n] of out_dt, 16-byte aligned.  May be the same buffer as
+ *               mul or residual; must not overlap the other inputs.
+ *   d_status    device int32; FP4Q_FLAG_OFFSETS if the offsets decrease or
+ *               leave [0, m] (nothing is written then), FP4Q_FLAG_TIMEOUT if a
+ *               wait inside the kernel gave up (y is then unspecified).
+ * An empty product (m, n or groups == 0) returns FP4Q_OK and enqueues nothing.
+ * E4M3 scale bytes are patterns without the sign bit, as the quantizers write
+ * them; a NaN pattern makes the outputs that it reaches NaN.
+ * The results of a call do not depend on other work or on the run: sums are
+ * taken in a fixed order.
+ * Errors: FP4Q_ERR_DTYPE (fmt, out_dt), FP4Q_ERR_SHAPE (negative sizes, k not
+ * a positive multiple of 32, m, groups * n or k above 2^31 - 1 - 256, a tensor
+ * that overflows), FP4Q_ERR_ARG (act, too many groups), FP4Q_ERR_NULL,
+ * FP4Q_ERR_ALIGN, FP4Q_ERR_CUDA.
+ */
+#define FP4Q_FLAG_OFFSETS 8             /* group offsets out of order or range */
+#define FP4Q_PRODUCT_GROUPS_MAX 1024
+
+typedef enum {
+    FP4Q_ACT_NONE = 0,
+    FP4Q_ACT_RELU = 1,
+    FP4Q_ACT_GELU = 2,                  /* z * Phi(z)                          */
+    FP4Q_ACT_GELU_TANH = 3,             /* its tanh approximation              */
+    FP4Q_ACT_SILU = 4                   /* z / (1 + exp(-z))                   */
+} fp4q_act;
+
+typedef struct {
+    const void* bias;
+    const void* mul;
+    const void* residual;
+    fp4q_act act;
+} fp4q_epilogue;
+
+fp4q_status fp4q_linear(fp4q_format fmt, const void* x, int64_t m, const uint8_t* w_codes,
+                        const uint8_t* w_scales, const float* w_global_scale, int64_t n, int64_t k,
+                        const fp4q_epilogue* ep, void* y, fp4q_dtype out_dt, int32_t* d_status,
+                        fp4q_stream_t stream);
+
+fp4q_status fp4q_linear_group(fp4q_format fmt, const void* x, int64_t m, const int32_t* offsets,
+                              int32_t groups, const uint8_t* w_codes, const uint8_t* w_scales,
+                              const float* w_global_scale, int64_t n, int64_t k, const fp4q_epilogue* ep,
+                              void* y, fp4q_dtype out_dt, int32_t* d_status, fp4q_stream_t stream);
+
+fp4q_status fp4q_matmul(fp4q_format fmt, const uint8_t* x_codes, const uint8_t* x_scales,
+                        const float* x_global_scale, int64_t m, const uint8_t* w_codes,
+                        const uint8_t* w_scales, const float* w_global_scale, int64_t n, int64_t k,
+                        const fp4q_epilogue* ep, void* y, fp4q_dtype out_dt, int32_t* d_status,
+                        fp4q_stream_t stream);
+
+fp4q_status fp4q_matmul_group(fp4q_format fmt, const uint8_t* x_codes, const uint8_t* x_scales,
+                              const float* x_global_scale, int64_t m, const int32_t* offsets, int32_t groups,
+                              const uint8_t* w_codes, const uint8_t* w_scales, const float* w_global_scale,
+                              int64_t n, int64_t k, const fp4q_epilogue* ep, void* y, fp4q_dtype out_dt,
+                              int32_t* d_status, fp4q_stream_t stream);
+
+/*
  * Diagnostic entry points: the device's element and scale rounding primitives
  * applied to n floats, so that they can be compared with a reference codec.
  *   fp4q_probe_e2m1: out[i] = E2M1 nibble of r[i] (sign<<3 | code).
