@@ -1,0 +1,281 @@
+// matmul.cu -- fp4q_matmul and fp4q_matmul_group: both operands FP4, on the
+// block-scaled tensor-core instructions of sm_100a.
+//
+// One thread block works on tiles of 128 features x BN tokens (product_tile.cuh)
+// in steps of 256 columns, in four roles that meet at mbarriers:
+//   warp 0     copies the codes of both operands (128-byte rows, swizzled) and
+//              the weight's tiled scales into a ring of STAGES steps;
+//   warps 2-3  copy the tokens' row-major scales into the tiled layout of the
+//              ring, 4 bytes (one row of a tile) at a time;
+//   warp 1     one thread moves a step's scales to tensor memory and issues
+//              four products of 64 columns;
+//   warps 4-7  take the accumulator to y.
+// The products are exact (2 x 2 significant bits, block scales of 4 x 4) and
+// summed in binary32 in tensor memory; the global scales multiply the sum.
+#include "launch.h"
+#include "product.h"
+#include "product_host.cuh"
+
+namespace fp4q {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kStepCols = 256;             // columns of a step: 128 bytes of codes
+constexpr int kMmaCols = 64;
+
+template <int BN> struct Config {
+    static constexpr int kTokenTiles = (BN + 127) / 128;            // scale tiles over the tokens
+    static constexpr int kW = 128 * 128, kX = BN * 128;             // bytes of a step
+    static constexpr int kWS = 4 * 512, kXS = kTokenTiles * 4 * 512;
+    static constexpr int kStage = kW + kX + kWS + kXS;
+    static constexpr int kStages = BN == 128 ? 6 : 4;
+    static constexpr int kAccs = BN <= 128 ? 2 : 1;
+    // tensor memory: accumulators, then per stage the scales of 4 products
+    static constexpr int kScaleCols = 4 * 4 * (1 + kTokenTiles);
+    static constexpr int kUsed = kAccs * BN + kStages * kScaleCols;
+    static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+    static constexpr bool kSplits = BN <= 64;
+    static constexpr int kPart = kSplits ? BN * 128 * 4 : 0;        // partial sums of a split tile
+    static constexpr int kSmem = kStages * kStage + kPart + 1024;
+    static constexpr int kResident = BN <= 32 ? 2 : 1;
+    static_assert(kUsed <= 512 && kCols * kResident <= 512, "tensor memory");
+    static_assert(kSmem <= 227 * 1024 && kStage % 1024 == 0, "shared memory");
+};
+
+template <bool MX, int BN, typename T>
+__global__ void __launch_bounds__(kThreads, Config<BN>::kResident)
+matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
+              const __grid_constant__ TileArgs a)
+{
+    using C = Config<BN>;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[2 * C::kStages + 2 * C::kAccs + 3];
+    __shared__ int before[FP4Q_PRODUCT_GROUPS_MAX + 1];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead_word, good_offsets;
+    volatile int* dead = &dead_word;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    uint8_t* ring = raw + (1024 - smem_u32(raw) % 1024) % 1024;
+    float* part = reinterpret_cast<float*>(ring + C::kStages * C::kStage);
+    const uint32_t ring0 = smem_u32(ring);
+    const uint32_t full = smem_u32(bars), empty = full + 8 * C::kStages, acc_full = empty + 8 * C::kStages,
+                   acc_empty = acc_full + 8 * C::kAccs, part_full = acc_empty + 8 * C::kAccs, part_empty = part_full + 8,
+                   drain = part_empty + 8;
+    const uint32_t rank = a.split > 1 ? cluster_rank() : 0;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            dead_word = 0;
+            for (int i = 0; i < C::kStages; ++i) {
+                mbar_init(full + 8 * i, 1 + 2);            // the copies, two warps of token scales
+                mbar_init(empty + 8 * i, 1);
+            }
+            for (int i = 0; i < C::kAccs; ++i) {
+                mbar_init(acc_full + 8 * i, 1);
+                mbar_init(acc_empty + 8 * i, 1);
+            }
+            mbar_init(part_full, a.split);
+            mbar_init(part_empty, a.split);
+            mbar_init(drain, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            tma_prefetch_desc(&w_map);
+            tma_prefetch_desc(&x_map);
+        }
+    } else if (warp == 1) {
+        tmem_alloc(smem_u32(&tmem_slot), C::kCols);
+    } else if (warp == 2) {
+        const bool ok = tile_table<BN>(a, before);
+        if (lane == 0) good_offsets = ok;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (a.split > 1) cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int64_t tiles = good_offsets ? (int64_t)before[a.groups] * a.n_tiles : 0;
+    if (!good_offsets && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, FP4Q_FLAG_OFFSETS);
+    const int64_t first_tile = blockIdx.x / a.split, tile_step = gridDim.x / a.split;
+    const int per_tile = MX ? 128 : 64;                    // columns of a scale tile
+    int k0, k1;
+    split_steps(a, (int)rank, k0, k1);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+                const Tile tl = tile_at<BN>(a, before, t);
+                const int wrow = (int)(tl.group * a.n) + tl.feature;
+                const uint8_t* ws = a.w_scales + tl.group * a.w_scale_stride +
+                                    (int64_t)(tl.feature / 128) * a.w_col_tiles * 512;
+                for (int k = k0; k < k1; ++k, ++it) {
+                    const uint32_t s = it % C::kStages;
+                    if (!(ok = mbar_wait(empty + 8 * s, (it / C::kStages & 1) ^ 1, dead))) break;
+                    const uint32_t at = ring0 + s * C::kStage, bar = full + 8 * s;
+                    const int c0 = k * (kStepCols / per_tile);
+                    const uint32_t sb = (uint32_t)min(kStepCols / per_tile, a.w_col_tiles - c0) * 512;
+                    mbar_expect(bar, C::kW + C::kX + sb);
+                    tma_load(at, &w_map, k * (kStepCols / 2), wrow, bar);
+                    tma_load(at + C::kW, &x_map, k * (kStepCols / 2), tl.row, bar);
+                    bulk_load(at + C::kW + C::kX, ws + (int64_t)c0 * 512, sb, bar);
+                }
+            }
+            if (*dead)                                     // copies in flight end before the block does
+                for (uint32_t i = it < C::kStages ? 0 : it - C::kStages; i < it; ++i)
+                    mbar_drain(full + 8 * (i % C::kStages), i / C::kStages & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t it = 0, n = 0;
+            bool ok = true;
+            for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ++n) {
+                const Tile tl = tile_at<BN>(a, before, t);
+                const uint32_t cols = min(BN, (tl.rows + 15) / 16 * 16);
+                const uint32_t ac = n % C::kAccs, acc = tmem + ac * BN;
+                if (!(ok = mbar_wait(acc_empty + 8 * ac, (n / C::kAccs & 1) ^ 1, dead))) break;
+                tc_fence_after();
+                for (int k = k0; k < k1; ++k, ++it) {
+                    const uint32_t s = it % C::kStages;
+                    if (!(ok = mbar_wait(full + 8 * s, it / C::kStages & 1, dead))) break;
+                    tc_fence_after();
+                    const uint32_t at = ring0 + s * C::kStage;
+                    const uint32_t sf = tmem + C::kAccs * BN + s * C::kScaleCols;
+                    const int parts = min(kStepCols / kMmaCols, (a.k - k * kStepCols + kMmaCols - 1) / kMmaCols);
+                    const int scale_tiles = MX ? (parts + 1) / 2 : parts;
+                    for (int i = 0; i < scale_tiles; ++i) {
+                        tc_copy_scales(sf + i * 4, desc_scales(at + C::kW + C::kX + i * 512));
+#pragma unroll
+                        for (int h = 0; h < C::kTokenTiles; ++h)
+                            tc_copy_scales(sf + 16 + i * 4 * C::kTokenTiles + h * 4,
+                                           desc_scales(at + C::kW + C::kX + C::kWS + (i * C::kTokenTiles + h) * 512));
+                    }
+                    for (int i = 0; i < parts; ++i) {
+                        const int st = MX ? i / 2 : i;
+                        tc_mma_fp4<MX>(acc, desc_k128(at + i * 32), desc_k128(at + C::kW + i * 32),
+                                       idesc_fp4(MX, cols, MX ? (i % 2) * 2 : 0), sf + st * 4,
+                                       sf + 16 + st * 4 * C::kTokenTiles, k > k0 || i > 0);
+                    }
+                    tc_commit(empty + 8 * s);
+                }
+                tc_commit(acc_full + 8 * ac);
+            }
+            if (*dead) {
+                tc_commit(drain);
+                mbar_drain(drain, 0);
+            }
+        }
+    } else if (warp < 4) {
+        // Token scales: thread i of the 64 takes rows i, i + 64, ...; a row's
+        // scales of one tile are 4 neighbouring bytes, at (r % 32) * 16 +
+        // (r / 32) * 4 of that tile.  A step is announced two steps later, when
+        // its copies have landed.
+        constexpr int kLag = 2;
+        const int i0 = threadIdx.x - 64;
+        const int64_t scols = a.k / (MX ? 32 : 16);
+        const bool words = scols % 4 == 0;                 // rows start on 4-byte boundaries
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+            const Tile tl = tile_at<BN>(a, before, t);
+            for (int k = k0; k < k1; ++k, ++it) {
+                const uint32_t s = it % C::kStages;
+                if (!(ok = mbar_wait(empty + 8 * s, (it / C::kStages & 1) ^ 1, dead))) break;
+                uint8_t* xs = ring + s * C::kStage + C::kW + C::kX + C::kWS;
+                const int64_t c0 = (int64_t)k * (kStepCols / per_tile) * 4;
+                for (int r = i0; r < BN; r += 64) {
+                    const int64_t row = tl.row + r;
+                    const bool in = row < a.m && r < tl.rows;
+                    const uint8_t* src = a.x_scales + (in ? row * scols : 0);
+#pragma unroll
+                    for (int i = 0; i < kStepCols / per_tile; ++i) {
+                        uint8_t* dst = xs + (i * C::kTokenTiles + r / 128) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4;
+                        const int64_t c = c0 + 4 * i;
+                        if (words) {
+                            const bool there = in && c < scols;
+                            cp_async4(smem_u32(dst), there ? src + c : a.x_scales, there ? 4 : 0);
+                        } else {
+                            uint32_t v = 0;
+                            for (int b = 0; b < 4; ++b)
+                                if (in && c + b < scols) v |= (uint32_t)__ldg(src + c + b) << (8 * b);
+                            *reinterpret_cast<uint32_t*>(dst) = v;
+                        }
+                    }
+                }
+                cp_async_commit();
+                if (it >= kLag) {
+                    cp_async_wait<kLag>();
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full + 8 * ((it - kLag) % C::kStages));
+                }
+            }
+        }
+        cp_async_wait<0>();
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0)
+            for (uint32_t i = it < kLag ? 0 : it - kLag; i < it; ++i) mbar_arrive(full + 8 * (i % C::kStages));
+    } else {
+        uint32_t n = 0;
+        bool ok = true;
+        for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ++n) {
+            const Tile tl = tile_at<BN>(a, before, t);
+            const uint32_t ac = n % C::kAccs, acc = tmem + ac * BN;
+            const float S = MX ? 1.f : a.w_S[tl.group] * *a.x_S;
+            ok = mbar_wait(acc_full + 8 * ac, n / C::kAccs & 1, dead);
+            tc_fence_after();
+            if (C::kSplits && a.split > 1) {
+                ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, n & 1, rank, dead,
+                                         acc_empty + 8 * ac) && ok;
+            } else {
+                if (ok) write_tile<T>(a, tl, acc, S);
+                tc_fence_before();
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (threadIdx.x == 128) mbar_arrive(acc_empty + 8 * ac);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_free(tmem, C::kCols);
+    if (threadIdx.x == 0 && *dead) atomicOr(a.status, FP4Q_FLAG_TIMEOUT);
+    if (a.split > 1) cluster_sync_all();       // a peer may still read this block's partial sums
+}
+
+}  // namespace
+
+template <bool MX, int BN, typename T> static cudaError_t launch_one(const Product& p, TileArgs& a, int split, cudaStream_t s)
+{
+    using C = Config<BN>;
+    auto kernel = matmul_kernel<MX, BN, T>;
+    CUtensorMap w_map, x_map;
+    cudaError_t e = byte_tile_map(&w_map, p.w, p.n * p.groups, p.k / 2, 128);
+    if (e == cudaSuccess) e = byte_tile_map(&x_map, p.x, p.m, p.k / 2, BN);
+    if (e != cudaSuccess) return e;
+    const int per_sm = resident_blocks_per_sm(reinterpret_cast<const void*>(kernel), kThreads, C::kSmem);
+    return launch_tiles(kernel, w_map, x_map, p, a, BN, split, per_sm, kThreads, C::kSmem, s);
+}
+
+template <bool MX, typename T> static cudaError_t launch_shape(const Product& p, cudaStream_t s)
+{
+    TileArgs a = tile_args(p, kStepCols, MX ? 128 : 64);
+    const TileShape shape = tile_shape(p, a.n_tiles, a.k_steps);
+    switch (shape.tokens) {
+    case 16: return launch_one<MX, 16, T>(p, a, shape.split, s);
+    case 32: return launch_one<MX, 32, T>(p, a, shape.split, s);
+    case 64: return launch_one<MX, 64, T>(p, a, shape.split, s);
+    case 128: return launch_one<MX, 128, T>(p, a, 1, s);
+    default: return launch_one<MX, 256, T>(p, a, 1, s);
+    }
+}
+
+cudaError_t launch_matmul(const Product& p, cudaStream_t s)
+{
+    if (p.mx) return p.out_bf16 ? launch_shape<true, __nv_bfloat16>(p, s) : launch_shape<true, float>(p, s);
+    return p.out_bf16 ? launch_shape<false, __nv_bfloat16>(p, s) : launch_shape<false, float>(p, s);
+}
+
+}  // namespace fp4q

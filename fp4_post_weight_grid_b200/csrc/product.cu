@@ -3,8 +3,7 @@
 // binary32 in shared memory and multiplied there.
 #include "device.cuh"
 #include "launch.h"
-#include "product.h"
-#include "product_epilogue.cuh"
+#include "product_host.cuh"
 
 namespace fp4q {
 
@@ -103,8 +102,83 @@ __global__ void __launch_bounds__(kThreads) product_kernel(Product p)
 
 }  // namespace
 
+namespace {
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder, looked up once (the library is not linked to the driver).
+EncodeTiled encoder()
+{
+    static const EncodeTiled fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeTiled>(f);
+    }();
+    return fn;
+}
+
+}  // namespace
+
+cudaError_t byte_tile_map(CUtensorMap* map, const void* base, int64_t rows, int64_t row_bytes, int box_rows)
+{
+    const EncodeTiled encode = encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    const cuuint32_t steps[2] = {1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, steps,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+TileArgs tile_args(const Product& p, int step_cols, int scale_tile_cols)
+{
+    TileArgs a{};
+    a.offsets = p.offsets;
+    a.n = p.n;
+    a.m = (int)p.m;
+    a.k = (int)p.k;
+    a.groups = p.groups;
+    a.n_tiles = (int)((p.n + 127) / 128);
+    a.k_steps = (int)((p.k + step_cols - 1) / step_cols);
+    a.split = 1;
+    a.w_col_tiles = (int)((p.k + scale_tile_cols - 1) / scale_tile_cols);
+    a.x_scales = p.x_scales;
+    a.x_S = p.x_S;
+    a.w_scales = p.w_scales;
+    a.w_S = p.w_S;
+    a.w_scale_stride = p.w_scale_stride;
+    a.ep = EpilogueArgs{p.ep.bias, p.ep.mul, p.ep.residual, p.y, (int)p.ep.act};
+    a.status = p.status;
+    return a;
+}
+
+TileShape tile_shape(const Product& p, int n_tiles, int k_steps)
+{
+    const int64_t rows = p.offsets ? (p.m + p.groups - 1) / p.groups : p.m;       // of a group, on average
+    const int64_t busy = p.offsets ? std::min<int64_t>(p.groups, p.m) : 1;
+    const int sms = sm_count();
+    TileShape t{16, 1};
+    while (t.tokens < 256 && t.tokens < rows) t.tokens *= 2;
+    auto tiles = [&] { return busy * ((rows + t.tokens - 1) / t.tokens) * n_tiles; };
+    while (t.tokens > 32 && tiles() < sms) t.tokens /= 2;
+    if (t.tokens <= 64) {
+        const int64_t slots = (int64_t)sms * (t.tokens <= 32 ? 2 : 1);
+        while (t.split < 8 && t.split * 2 <= k_steps && tiles() * t.split * 2 <= slots) t.split *= 2;
+    }
+    return t;
+}
+
 cudaError_t launch_product(const Product& p, cudaStream_t s)
 {
+    if (p.packed) return launch_matmul(p, s);
     const int64_t nt = (p.n + kTile - 1) / kTile, mt = (p.m + kTile - 1) / kTile;
     const dim3 grid((unsigned)(nt < 65535 ? nt : 65535), (unsigned)(mt < 1024 ? mt : 1024), (unsigned)p.groups);
     if (p.out_bf16)

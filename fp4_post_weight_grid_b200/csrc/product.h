@@ -29,6 +29,8 @@ struct Product {
     int32_t* status;
 };
 
+// All checks are done; m, n and groups are positive.
 cudaError_t launch_product(const Product& p, cudaStream_t s);
+cudaError_t launch_matmul(const Product& p, cudaStream_t s);      // packed
 
 }  // namespace fp4q

@@ -1,0 +1,52 @@
+// product_host.cuh -- host side of the tensor-core kernels of the products.
+#pragma once
+
+#include <algorithm>
+
+#include "launch.h"
+#include "product.h"
+#include "product_tile.cuh"
+
+namespace fp4q {
+
+// Tensor map of a [rows][row_bytes] byte matrix, tiles of `box_rows` rows x 128
+// bytes under the 128-byte swizzle; reads past the edges give zeros.
+cudaError_t byte_tile_map(CUtensorMap* map, const void* base, int64_t rows, int64_t row_bytes, int box_rows);
+
+// The kernel arguments that do not depend on the tile shape.
+TileArgs tile_args(const Product& p, int step_cols, int scale_tile_cols);
+
+struct TileShape {
+    int tokens;      // BN: 16, 32, 64, 128 or 256
+    int split;       // thread blocks that share a tile's K
+};
+TileShape tile_shape(const Product& p, int n_tiles, int k_steps);
+
+// One launch over all tiles: as many clusters of `split` thread blocks as are
+// resident at once (or as there are tiles, if fewer), each striding over the
+// tiles.  A grouped call knows only how many tiles there can be at most.
+template <typename Kernel>
+cudaError_t launch_tiles(Kernel kernel, const CUtensorMap& w_map, const CUtensorMap& x_map, const Product& p,
+                         TileArgs& a, int tokens, int split, int per_sm, int threads, size_t smem, cudaStream_t s)
+{
+    a.split = split;
+    int64_t token_tiles = (p.m + tokens - 1) / tokens;
+    if (p.offsets) token_tiles = std::min<int64_t>(p.m, p.m / tokens + p.groups);
+    const int64_t slots = std::max<int64_t>(1, (int64_t)sm_count() * per_sm / split);
+    const int64_t clusters = std::min<int64_t>(token_tiles * a.n_tiles, slots);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(clusters * split));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, w_map, x_map, a);
+}
+
+}  // namespace fp4q

@@ -195,7 +195,9 @@ def _bound(z, absz, k, act, out, bias, mul, residual):
 
 SHAPES = [(1, 1, 32), (1, 128, 64), (2, 130, 96), (8, 64, 256), (17, 96, 160), (31, 257, 288), (64, 128, 544),
           (65, 200, 512), (129, 257, 1056), (256, 384, 256), (300, 1000, 1056), (1, 1024, 4096), (5, 333, 8192),
-          (513, 130, 320)]
+          (513, 130, 320),
+          # enough rows of W that the wider token tiles are chosen, their last one partly filled
+          (40, 19073, 96), (60, 19073, 352), (120, 19073, 288), (300, 19073, 96), (257, 19000, 1056)]
 
 
 @pytest.mark.parametrize("form,fmt", FORMS, ids=form_ids)
@@ -220,6 +222,12 @@ def test_exact_groups(form, fmt, counts, before, behind, n, k):
         pytest.skip("one size of the many groups is enough")
     Problem(form, fmt, 0, n, k, counts=counts, before=before, behind=behind, exact=True, seed=n + len(counts),
             bias=True).check(exact=True)
+
+
+@pytest.mark.parametrize("form,fmt", FORMS, ids=form_ids)
+@pytest.mark.parametrize("counts", [[300, 0, 513, 100], [90, 130], [33, 40, 61]])
+def test_exact_groups_of_wide_tiles(form, fmt, counts):
+    Problem(form, fmt, 0, 10001, 352, counts=counts, behind=3, exact=True, bias=True).check(exact=True)
 
 
 @pytest.mark.parametrize("form,fmt", FORMS, ids=form_ids)
