@@ -18,7 +18,7 @@ ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp4q.so")
 SOURCES = ["api.cu", "absmax.cu", "nvfp4.cu", "mxfp4.cu", "dequant.cu", "batch.cu", "dynamic.cu", "layout.cu", "focus.cu", "gptq.cu",
-           "product.cu", "matmul.cu"]
+           "product.cu", "matmul.cu", "linear.cu"]
 HEADERS = ["device.cuh", "launch.h", "screen.cuh", "nvfp4_block.cuh", "mxfp4_block.cuh", "batch.h", "wait.cuh",
            "product.h", "product_epilogue.cuh", "tc.cuh", "product_tile.cuh",
            "product_host.cuh"]
@@ -48,7 +48,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(os.path.join(HERE, "_build"), exist_ok=True)
-    cmd = [nvcc_path(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "--fmad=false", "-Xptxas", "--fmad=false",
+    cmd = [nvcc_path(), "-O3", "-std=c++17", "--threads", "0", *ARCH, "-lineinfo", "--fmad=false", "-Xptxas", "--fmad=false",
            "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-v",
            "-I", os.path.join(ROOT, "include"),
            *[os.path.join(SRC, s) for s in SOURCES], "-o", LIB + ".tmp"]

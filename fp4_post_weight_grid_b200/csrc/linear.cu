@@ -1,0 +1,368 @@
+// linear.cu -- fp4q_linear and fp4q_linear_group: bf16 activations times FP4
+// weights on the bf16 tensor cores of sm_100a.
+//
+// q * s of an NVFP4 element has at most 2 + 4 significant bits and q * 2^e of an
+// MXFP4 element 2, so a decoded weight is a bf16 value and the product needs no
+// rounding of the weight.  The weight is decoded once per tile, by the thread
+// that owns its row, from shared memory straight into tensor memory, where the
+// tensor core takes it as the operand that fills the 128 lanes; x goes from
+// global to shared memory as it is.  Roles of a thread block's warps, meeting
+// at mbarriers:
+//   warp 0     copies codes and scales into a ring (steps of 256 columns);
+//   warp 3     copies x into another (steps of 64 columns, 128-byte rows, swizzled);
+//   warp 1     one thread issues the products, 4 of 16 columns per step of x;
+//   warp 2     the tile table, then idle;
+//   warps 4..  DQ groups of four decode, a step of 64 columns at a time;
+//   the last 4 take the accumulator to y (product_tile.cuh).
+#include "product_host.cuh"
+
+namespace fp4q {
+
+namespace {
+
+constexpr int kStepCols = 256;             // columns of a step of W: 128 bytes of codes
+constexpr int kSubCols = 64;               // columns of a step of x and of decoded W
+constexpr int kASteps = 4;                 // decoded steps in tensor memory
+constexpr int kACols = kSubCols / 2;       // columns of tensor memory per decoded step
+
+template <int BN> struct Config {
+    static constexpr int kW = 128 * 128, kWStage = kW + 4 * 512, kX = BN * 128;
+    static constexpr int kWStages = BN >= 256 ? 3 : BN >= 128 ? 5 : BN >= 64 ? 7 : 4;
+    static constexpr int kXStages = BN >= 256 ? 5 : BN >= 64 ? 6 : BN >= 32 ? 4 : 8;
+    static constexpr int kAccs = BN <= 128 ? 2 : 1;
+    static constexpr int kDq = BN <= 32 ? 1 : 2;                    // groups of four decoding warps
+    static constexpr int kThreads = (4 + 4 * kDq + 4) * 32;
+    static constexpr int kUsed = kAccs * BN + kASteps * kACols;
+    static constexpr int kCols = kUsed <= 256 ? 256 : 512;
+    static constexpr bool kSplits = BN <= 64;
+    static constexpr int kPart = kSplits ? BN * 128 * 4 : 0;        // partial sums of a split tile
+    static constexpr int kSmem = kWStages * kWStage + kXStages * kX + kPart + 1024;
+    static constexpr int kResident = BN <= 32 ? 2 : 1;
+    static_assert(kUsed <= 512 && kCols * kResident <= 512, "tensor memory");
+    static_assert(kSmem <= 222 * 1024 && kWStage % 1024 == 0 && kX % 1024 == 0, "shared memory");
+};
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Eight codes -> four pairs of bf16 in column order, each q * 2^-126: the three
+// magnitude bits of a code put where bf16 keeps the low exponent bits and the
+// first mantissa bit are its value under an exponent bias of 127 instead of 1
+// (the code 1/2 becomes a subnormal, which the multiplication takes exactly).
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t scale, uint32_t* out)
+{
+    const uint32_t up = w << 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        // high byte of the low half: the low nibble of byte j, of the high half: the high nibble
+        const uint32_t p = __byte_perm(up, w, j | j << 4 | (4 + j) << 8 | (4 + j) << 12);
+        out[j] = mul_bf16x2((p & 0x80008000u) | ((p >> 6) & 0x01C001C0u), scale);
+    }
+}
+
+// The factor for decode8 of an E4M3 byte, in both halves: s * 2^119 (the
+// decoded weight is q * s * 2^-7, in range for every q and s).
+__device__ __forceinline__ uint32_t nv_factor(uint32_t byte)
+{
+    const uint32_t h = (byte & 0x7F) << 4, both = h | h << 16;             // s * 2^-120
+    const uint32_t f = mul_bf16x2(mul_bf16x2(both, 0x7F007F00u), 0x77807780u);   // * 2^127 * 2^112
+    return (byte & 0x7F) == 0x7F ? 0x7FC07FC0u : f;
+}
+// Of an E8M0 byte: 2^(b-127-2+126) up to b = 130, where the product is
+// q * 2^(b-129); what is above 130 is left to mx_rest.
+__device__ __forceinline__ uint32_t mx_factor(uint32_t byte)
+{
+    const uint32_t h = (min(byte, 130u) + 124) << 7;
+    return h | h << 16;
+}
+__device__ __forceinline__ uint32_t mx_rest(uint32_t byte)
+{
+    const uint32_t h = byte == 255 ? 0x7FC0u : (byte - 130 + 127) << 7;
+    return h | h << 16;
+}
+
+// D[128][N] (+)= A[128][16] * B[N][16]^T, bf16, A in tensor memory.
+__device__ __forceinline__ void tc_mma_bf16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "r"((uint32_t)add)
+        : "memory");
+}
+// Binary32 sums (1 << 4) of bf16 operands (1 << 7, 1 << 10), both K-major, 128 x n.
+__device__ __forceinline__ uint32_t idesc_bf16(uint32_t n)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+template <bool MX, int BN, typename T>
+__global__ void __launch_bounds__(Config<BN>::kThreads, Config<BN>::kResident)
+linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
+              const __grid_constant__ TileArgs a)
+{
+    using C = Config<BN>;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[2 * (C::kWStages + C::kXStages + kASteps + C::kAccs) + 3];
+    __shared__ int before[FP4Q_PRODUCT_GROUPS_MAX + 1];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int dead_word, good_offsets;
+    volatile int* dead = &dead_word;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    uint8_t* w_ring = raw + (1024 - smem_u32(raw) % 1024) % 1024;
+    uint8_t* x_ring = w_ring + C::kWStages * C::kWStage;
+    float* part = reinterpret_cast<float*>(x_ring + C::kXStages * C::kX);
+    const uint32_t w_full = smem_u32(bars), w_empty = w_full + 8 * C::kWStages, x_full = w_empty + 8 * C::kWStages,
+                   x_empty = x_full + 8 * C::kXStages, a_full = x_empty + 8 * C::kXStages, a_empty = a_full + 8 * kASteps,
+                   acc_full = a_empty + 8 * kASteps, acc_empty = acc_full + 8 * C::kAccs,
+                   part_full = acc_empty + 8 * C::kAccs, part_empty = part_full + 8, drain = part_empty + 8;
+    const uint32_t rank = a.split > 1 ? cluster_rank() : 0;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            dead_word = 0;
+            for (int i = 0; i < C::kWStages; ++i) {
+                mbar_init(w_full + 8 * i, 1);
+                mbar_init(w_empty + 8 * i, 4 * C::kDq);
+            }
+            for (int i = 0; i < C::kXStages; ++i) {
+                mbar_init(x_full + 8 * i, 1);
+                mbar_init(x_empty + 8 * i, 1);
+            }
+            for (int i = 0; i < kASteps; ++i) {
+                mbar_init(a_full + 8 * i, 4);
+                mbar_init(a_empty + 8 * i, 1);
+            }
+            for (int i = 0; i < C::kAccs; ++i) {
+                mbar_init(acc_full + 8 * i, 1);
+                mbar_init(acc_empty + 8 * i, 1);
+            }
+            mbar_init(part_full, a.split);
+            mbar_init(part_empty, a.split);
+            mbar_init(drain, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            tma_prefetch_desc(&w_map);
+            tma_prefetch_desc(&x_map);
+        }
+    } else if (warp == 1) {
+        tmem_alloc(smem_u32(&tmem_slot), C::kCols);
+    } else if (warp == 2) {
+        const bool ok = tile_table<BN>(a, before);
+        if (lane == 0) good_offsets = ok;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (a.split > 1) cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot, a_tmem = tmem + C::kAccs * BN;
+    const int64_t tiles = good_offsets ? (int64_t)before[a.groups] * a.n_tiles : 0;
+    if (!good_offsets && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, FP4Q_FLAG_OFFSETS);
+    const int64_t first_tile = blockIdx.x / a.split, tile_step = gridDim.x / a.split;
+    constexpr int kScaleTile = MX ? 128 : 64;              // columns of a scale tile
+    int k0, k1;
+    split_steps(a, (int)rank, k0, k1);
+    // sub-steps of 64 columns of step k
+    auto subs = [&](int k) { return min(kStepCols / kSubCols, (a.k - k * kStepCols + kSubCols - 1) / kSubCols); };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+                const Tile tl = tile_at<BN>(a, before, t);
+                const int wrow = (int)(tl.group * a.n) + tl.feature;
+                const uint8_t* ws = a.w_scales + tl.group * a.w_scale_stride +
+                                    (int64_t)(tl.feature / 128) * a.w_col_tiles * 512;
+                for (int k = k0; k < k1; ++k, ++it) {
+                    const uint32_t s = it % C::kWStages;
+                    if (!(ok = mbar_wait(w_empty + 8 * s, (it / C::kWStages & 1) ^ 1, dead))) break;
+                    const uint32_t at = smem_u32(w_ring) + s * C::kWStage, bar = w_full + 8 * s;
+                    const int c0 = k * (kStepCols / kScaleTile);
+                    const uint32_t sb = (uint32_t)min(kStepCols / kScaleTile, a.w_col_tiles - c0) * 512;
+                    mbar_expect(bar, C::kW + sb);
+                    tma_load(at, &w_map, k * (kStepCols / 2), wrow, bar);
+                    bulk_load(at + C::kW, ws + (int64_t)c0 * 512, sb, bar);
+                }
+            }
+            if (*dead)                                     // copies in flight end before the block does
+                for (uint32_t i = it < C::kWStages ? 0 : it - C::kWStages; i < it; ++i)
+                    mbar_drain(w_full + 8 * (i % C::kWStages), i / C::kWStages & 1);
+        }
+    } else if (warp == 3) {
+        if (lane == 0) {
+            uint32_t j = 0;
+            bool ok = true;
+            for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+                const Tile tl = tile_at<BN>(a, before, t);
+                const int c1 = min(a.k, k1 * kStepCols);
+                for (int c = k0 * kStepCols; c < c1; c += kSubCols, ++j) {
+                    const uint32_t s = j % C::kXStages;
+                    if (!(ok = mbar_wait(x_empty + 8 * s, (j / C::kXStages & 1) ^ 1, dead))) break;
+                    mbar_expect(x_full + 8 * s, C::kX);
+                    tma_load(smem_u32(x_ring) + s * C::kX, &x_map, c * 2, tl.row, x_full + 8 * s);
+                }
+            }
+            if (*dead)
+                for (uint32_t i = j < C::kXStages ? 0 : j - C::kXStages; i < j; ++i)
+                    mbar_drain(x_full + 8 * (i % C::kXStages), i / C::kXStages & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t j = 0, n = 0;
+            bool ok = true;
+            for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ++n) {
+                const Tile tl = tile_at<BN>(a, before, t);
+                const uint32_t idesc = idesc_bf16(min(BN, (tl.rows + 15) / 16 * 16));
+                const uint32_t ac = n % C::kAccs, acc = tmem + ac * BN;
+                if (!(ok = mbar_wait(acc_empty + 8 * ac, (n / C::kAccs & 1) ^ 1, dead))) break;
+                tc_fence_after();
+                const int total = (min(a.k, k1 * kStepCols) - k0 * kStepCols + kSubCols - 1) / kSubCols;
+                for (int i = 0; i < total; ++i, ++j) {
+                    const uint32_t as = j % kASteps, xs = j % C::kXStages;
+                    if (!(ok = mbar_wait(x_full + 8 * xs, j / C::kXStages & 1, dead) &&
+                               mbar_wait(a_full + 8 * as, j / kASteps & 1, dead)))
+                        break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < kSubCols / 16; ++c)
+                        tc_mma_bf16(acc, a_tmem + as * kACols + c * 8,
+                                    desc_k128(smem_u32(x_ring) + xs * C::kX + c * 32), idesc, i > 0 || c > 0);
+                    tc_commit(a_empty + 8 * as);
+                    tc_commit(x_empty + 8 * xs);
+                }
+                tc_commit(acc_full + 8 * ac);
+            }
+            if (*dead) {
+                tc_commit(drain);
+                mbar_drain(drain, 0);
+            }
+        }
+    } else if (warp >= 4 && warp < 4 + 4 * C::kDq) {
+        const int group = (warp - 4) / 4, quarter = warp % 4, row = quarter * 32 + lane;
+        uint32_t it = 0, j = 0;
+        bool ok = true;
+        for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+            for (int k = k0; ok && k < k1; ++k, ++it) {
+                const uint32_t s = it % C::kWStages;
+                if (!(ok = mbar_wait(w_full + 8 * s, it / C::kWStages & 1, dead))) break;
+                const uint8_t* codes = w_ring + s * C::kWStage + row * 128;
+                const uint8_t* scales = w_ring + s * C::kWStage + C::kW + lane * 16 + quarter * 4;
+                const int n = subs(k);
+                for (int i = 0; i < n; ++i, ++j) {
+                    if (C::kDq > 1 && i % C::kDq != group) continue;
+                    const uint4 c0 = *reinterpret_cast<const uint4*>(codes + ((2 * i) ^ (row & 7)) * 16);
+                    const uint4 c1 = *reinterpret_cast<const uint4*>(codes + ((2 * i + 1) ^ (row & 7)) * 16);
+                    const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + (MX ? i / 2 : i) * 512);
+                    const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                    uint32_t r[32];
+                    if (MX) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t b = (sc >> (16 * (i & 1) + 8 * h)) & 255, f = mx_factor(b);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) decode8(w[4 * h + q], f, r + 16 * h + 4 * q);
+                            if (b > 130) {
+                                const uint32_t f2 = mx_rest(b);
+#pragma unroll
+                                for (int q = 0; q < 16; ++q) r[16 * h + q] = mul_bf16x2(r[16 * h + q], f2);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            const uint32_t f = nv_factor((sc >> (8 * h)) & 255);
+                            decode8(w[2 * h], f, r + 8 * h);
+                            decode8(w[2 * h + 1], f, r + 8 * h + 4);
+                        }
+                    }
+                    const uint32_t as = j % kASteps;
+                    if (!(ok = mbar_wait(a_empty + 8 * as, (j / kASteps & 1) ^ 1, dead))) break;
+                    tc_fence_after();
+                    tmem_store32(a_tmem + as * kACols + ((uint32_t)quarter << 21), r);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(a_full + 8 * as);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(w_empty + 8 * s);
+            }
+        }
+    } else if (warp >= 4 + 4 * C::kDq) {
+        uint32_t n = 0;
+        bool ok = true;
+        for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ++n) {
+            const Tile tl = tile_at<BN>(a, before, t);
+            const uint32_t ac = n % C::kAccs, acc = tmem + ac * BN;
+            const float S = MX ? 4.f : a.w_S[tl.group] * 128.f;        // the decoded weights are scaled down
+            ok = mbar_wait(acc_full + 8 * ac, n / C::kAccs & 1, dead);
+            tc_fence_after();
+            if (C::kSplits && a.split > 1) {
+                ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, n & 1, rank, dead,
+                                         acc_empty + 8 * ac) && ok;
+            } else {
+                if (ok) write_tile<T>(a, tl, acc, S);
+                tc_fence_before();
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (warp % 4 == 0 && lane == 0) mbar_arrive(acc_empty + 8 * ac);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_free(tmem, C::kCols);
+    if (threadIdx.x == 0 && *dead) atomicOr(a.status, FP4Q_FLAG_TIMEOUT);
+    if (a.split > 1) cluster_sync_all();       // a peer may still read this block's partial sums
+}
+
+}  // namespace
+
+template <bool MX, int BN, typename T> static cudaError_t launch_one(const Product& p, TileArgs& a, int split, cudaStream_t s)
+{
+    using C = Config<BN>;
+    auto kernel = linear_kernel<MX, BN, T>;
+    CUtensorMap w_map, x_map;
+    cudaError_t e = byte_tile_map(&w_map, p.w, p.n * p.groups, p.k / 2, 128);
+    if (e == cudaSuccess) e = byte_tile_map(&x_map, p.x, p.m, p.k * 2, BN);
+    if (e != cudaSuccess) return e;
+    const int per_sm = resident_blocks_per_sm(reinterpret_cast<const void*>(kernel), C::kThreads, C::kSmem);
+    return launch_tiles(kernel, w_map, x_map, p, a, BN, split, per_sm, C::kThreads, C::kSmem, s);
+}
+
+template <bool MX, typename T> static cudaError_t launch_shape(const Product& p, cudaStream_t s)
+{
+    TileArgs a = tile_args(p, kStepCols, MX ? 128 : 64);
+    const TileShape shape = tile_shape(p, a.n_tiles, a.k_steps);
+    switch (shape.tokens) {
+    case 16: return launch_one<MX, 16, T>(p, a, shape.split, s);
+    case 32: return launch_one<MX, 32, T>(p, a, shape.split, s);
+    case 64: return launch_one<MX, 64, T>(p, a, shape.split, s);
+    case 128: return launch_one<MX, 128, T>(p, a, 1, s);
+    default: return launch_one<MX, 256, T>(p, a, 1, s);
+    }
+}
+
+cudaError_t launch_linear(const Product& p, cudaStream_t s)
+{
+    if (p.mx) return p.out_bf16 ? launch_shape<true, __nv_bfloat16>(p, s) : launch_shape<true, float>(p, s);
+    return p.out_bf16 ? launch_shape<false, __nv_bfloat16>(p, s) : launch_shape<false, float>(p, s);
+}
+
+}  // namespace fp4q

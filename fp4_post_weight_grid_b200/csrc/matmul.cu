@@ -29,7 +29,7 @@ template <int BN> struct Config {
     static constexpr int kW = 128 * 128, kX = BN * 128;             // bytes of a step
     static constexpr int kWS = 4 * 512, kXS = kTokenTiles * 4 * 512;
     static constexpr int kStage = kW + kX + kWS + kXS;
-    static constexpr int kStages = BN == 128 ? 6 : 4;
+    static constexpr int kStages = BN == 128 ? 6 : BN == 32 ? 3 : 4;
     static constexpr int kAccs = BN <= 128 ? 2 : 1;
     // tensor memory: accumulators, then per stage the scales of 4 products
     static constexpr int kScaleCols = 4 * 4 * (1 + kTokenTiles);

@@ -31,6 +31,7 @@ struct Product {
 
 // All checks are done; m, n and groups are positive.
 cudaError_t launch_product(const Product& p, cudaStream_t s);
-cudaError_t launch_matmul(const Product& p, cudaStream_t s);      // packed
+cudaError_t launch_linear(const Product& p, cudaStream_t s);      // bf16 x
+cudaError_t launch_matmul(const Product& p, cudaStream_t s);      // packed x
 
 }  // namespace fp4q
