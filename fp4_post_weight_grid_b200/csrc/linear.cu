@@ -27,7 +27,7 @@ constexpr int kACols = kSubCols / 2;       // columns of tensor memory per decod
 
 template <int BN> struct Config {
     static constexpr int kW = 128 * 128, kWStage = kW + 4 * 512, kX = BN * 128;
-    static constexpr int kWStages = BN >= 256 ? 3 : BN >= 128 ? 5 : BN >= 64 ? 7 : 4;
+    static constexpr int kWStages = BN >= 256 ? 2 : BN >= 128 ? 5 : BN >= 64 ? 7 : 4;
     static constexpr int kXStages = BN >= 256 ? 5 : BN >= 64 ? 6 : BN >= 32 ? 4 : 8;
     static constexpr int kAccs = BN <= 128 ? 2 : 1;
     static constexpr int kDq = BN <= 32 ? 1 : 2;                    // groups of four decoding warps
@@ -35,7 +35,7 @@ template <int BN> struct Config {
     static constexpr int kUsed = kAccs * BN + kASteps * kACols;
     static constexpr int kCols = kUsed <= 256 ? 256 : 512;
     static constexpr bool kSplits = BN <= 64;
-    static constexpr int kPart = kSplits ? BN * 128 * 4 : 0;        // partial sums of a split tile
+    static constexpr int kPart = (kSplits ? BN : 32) * kPartRow * 4;        // sums on their way to y
     static constexpr int kSmem = kWStages * kWStage + kXStages * kX + kPart + 1024;
     static constexpr int kResident = BN <= 32 ? 2 : 1;
     static_assert(kUsed <= 512 && kCols * kResident <= 512, "tensor memory");
@@ -317,9 +317,9 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, n & 1, rank, dead,
                                          acc_empty + 8 * ac) && ok;
             } else {
-                if (ok) write_tile<T>(a, tl, acc, S);
+                if (ok) write_tile<T, Chunk<T, BN>::kTokens>(a, tl, acc, S, part);
                 tc_fence_before();
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                tile_bar();
                 if (warp % 4 == 0 && lane == 0) mbar_arrive(acc_empty + 8 * ac);
             }
         }

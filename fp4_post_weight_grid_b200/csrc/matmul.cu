@@ -29,14 +29,14 @@ template <int BN> struct Config {
     static constexpr int kW = 128 * 128, kX = BN * 128;             // bytes of a step
     static constexpr int kWS = 4 * 512, kXS = kTokenTiles * 4 * 512;
     static constexpr int kStage = kW + kX + kWS + kXS;
-    static constexpr int kStages = BN == 128 ? 6 : BN == 32 ? 3 : 4;
+    static constexpr int kStages = BN == 128 ? 5 : BN == 32 || BN == 256 ? 3 : 4;
     static constexpr int kAccs = BN <= 128 ? 2 : 1;
     // tensor memory: accumulators, then per stage the scales of 4 products
     static constexpr int kScaleCols = 4 * 4 * (1 + kTokenTiles);
     static constexpr int kUsed = kAccs * BN + kStages * kScaleCols;
     static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     static constexpr bool kSplits = BN <= 64;
-    static constexpr int kPart = kSplits ? BN * 128 * 4 : 0;        // partial sums of a split tile
+    static constexpr int kPart = (kSplits ? BN : 32) * kPartRow * 4;        // sums on their way to y
     static constexpr int kSmem = kStages * kStage + kPart + 1024;
     static constexpr int kResident = BN <= 32 ? 2 : 1;
     static_assert(kUsed <= 512 && kCols * kResident <= 512, "tensor memory");
@@ -230,9 +230,9 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, n & 1, rank, dead,
                                          acc_empty + 8 * ac) && ok;
             } else {
-                if (ok) write_tile<T>(a, tl, acc, S);
+                if (ok) write_tile<T, Chunk<T, BN>::kTokens>(a, tl, acc, S, part);
                 tc_fence_before();
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                tile_bar();
                 if (threadIdx.x == 128) mbar_arrive(acc_empty + 8 * ac);
             }
         }

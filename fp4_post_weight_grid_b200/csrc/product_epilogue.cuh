@@ -18,6 +18,11 @@ struct EpilogueArgs {
     int act;
 };
 
+// Outputs that one thread finishes together: 16 bytes of y.
+template <typename T> struct Lanes {
+    static constexpr int kCount = 16 / sizeof(T);
+};
+
 template <typename T> __device__ __forceinline__ float to_f32(T v);
 template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -25,36 +30,109 @@ template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// The GELUs in the forms without cancellation for negative z: Phi(z) =
-// erfc(-z/sqrt 2)/2, and 1 + tanh(u) = 2/(1 + exp(-2u)).  A NaN stays a NaN
-// in every one of them.
-__device__ __forceinline__ float activate(float z, int act)
+__device__ __forceinline__ void unpack16(const uint4& u, float (&v)[4])
 {
-    switch (act) {
-    case FP4Q_ACT_RELU:
-        return z < 0.f ? 0.f : z;
-    case FP4Q_ACT_GELU:
-        return 0.5f * z * erfcf(z * -0.70710678f);
-    case FP4Q_ACT_GELU_TANH:
-        return z / (1.f + expf(-1.59576912f * (z + 0.044715f * z * z * z)));
-    case FP4Q_ACT_SILU:
-        return z / (1.f + expf(-z));
-    default:
-        return z;
+    v[0] = __uint_as_float(u.x);
+    v[1] = __uint_as_float(u.y);
+    v[2] = __uint_as_float(u.z);
+    v[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ void unpack16(const uint4& u, float (&v)[8])
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack16(const float (&v)[4])
+{
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+__device__ __forceinline__ uint4 pack16(const float (&v)[8])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The GELUs in the forms without cancellation for negative z: Phi(z) =
+// erfc(-z/sqrt 2)/2, and 1 + tanh(u) = 2/(1 + exp(-2u)).  The hardware
+// exponential and division (a few units in the last place of binary32; the
+// exponential's grow with its argument where the result vanishes) keep the
+// activation below the cost of the product.  A NaN stays a NaN in every one.
+template <int N> __device__ __forceinline__ void activate(float (&z)[N], int act)
+{
+    if (act == FP4Q_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = __fdividef(z[i], 1.f + __expf(-z[i]));
+    } else if (act == FP4Q_ACT_GELU_TANH) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            z[i] = __fdividef(z[i], 1.f + __expf(-1.59576912f * (z[i] + 0.044715f * z[i] * z[i] * z[i])));
+    } else if (act == FP4Q_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = 0.5f * z[i] * erfcf(z[i] * -0.70710678f);
+    } else if (act == FP4Q_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = z[i] < 0.f ? 0.f : z[i];
     }
 }
 
-// One output element.  mul and residual may alias y: the element is read by
-// the thread that then writes it.
-template <typename T>
-__device__ __forceinline__ void finish(const EpilogueArgs& e, float acc, float S, float bias, bool has_bias, int64_t at)
+// What the 16 bytes of y at element `at` need from mul and residual, loaded
+// ahead of their use.  y may be either of them: an element is read by the
+// thread that then writes it.  `whole`: all of them exist and are aligned.
+template <typename T> struct Extra {
+    uint4 mul, residual;
+};
+template <typename T> __device__ __forceinline__ uint4 load_lanes(const void* p, int64_t at, int count, bool whole)
 {
-    float z = acc * S;
-    if (has_bias) z += bias;
-    z = activate(z, e.act);
-    if (e.mul) z *= to_f32<T>(static_cast<const T*>(e.mul)[at]);
-    if (e.residual) z += to_f32<T>(static_cast<const T*>(e.residual)[at]);
-    static_cast<T*>(e.y)[at] = from_f32<T>(z);
+    const T* q = static_cast<const T*>(p) + at;
+    if (whole) return *reinterpret_cast<const uint4*>(q);
+    float v[Lanes<T>::kCount];
+#pragma unroll
+    for (int i = 0; i < Lanes<T>::kCount; ++i) v[i] = i < count ? to_f32<T>(q[i]) : 0.f;
+    return pack16(v);
+}
+template <typename T>
+__device__ __forceinline__ Extra<T> load_extra(const EpilogueArgs& e, int64_t at, int count, bool whole)
+{
+    Extra<T> x;
+    if (e.mul) x.mul = load_lanes<T>(e.mul, at, count, whole);
+    if (e.residual) x.residual = load_lanes<T>(e.residual, at, count, whole);
+    return x;
+}
+// bias: of the same elements, zeros where there is none (adding zero changes
+// no value but the sign of a zero).
+template <typename T, int N>
+__device__ __forceinline__ void finish(const EpilogueArgs& e, float (&z)[N], const float (&bias)[N], const Extra<T>& x,
+                                       int64_t at, int count, bool whole)
+{
+    static_assert(N == Lanes<T>::kCount, "16 bytes");
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] += bias[i];
+    if (e.act != FP4Q_ACT_NONE) activate(z, e.act);
+    float v[N];
+    if (e.mul) {
+        unpack16(x.mul, v);
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] *= v[i];
+    }
+    if (e.residual) {
+        unpack16(x.residual, v);
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] += v[i];
+    }
+    T* q = static_cast<T*>(e.y) + at;
+    if (whole) {
+        *reinterpret_cast<uint4*>(q) = pack16(z);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < count) q[i] = from_f32<T>(z[i]);
+    }
 }
 
 }  // namespace fp4q

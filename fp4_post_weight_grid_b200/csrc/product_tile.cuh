@@ -107,31 +107,96 @@ __device__ __forceinline__ void split_steps(const TileArgs& a, int rank, int& fi
 }
 
 // From the accumulator (lane = feature, column = token) to y, by four warps
-// that each own a quarter of the lanes.  A thread keeps its feature, so a
-// store of a warp covers 32 neighbouring features of one token.
-template <typename T>
-__device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uint32_t acc, float S)
+// that each own a quarter of the lanes, kChunk tokens at a time through
+// shared memory: a thread writes its feature's sums of the chunk there (rows
+// of 132 floats, so that neither side has bank conflicts) and then finishes 16
+// bytes of y at a time, whose mul and residual it asked for before.
+constexpr int kPartRow = 132;
+template <typename T, int BN> struct Chunk {
+    static constexpr int kTokens = BN < 4 * Lanes<T>::kCount ? BN : 4 * Lanes<T>::kCount;
+};
+
+__device__ __forceinline__ void tile_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ void to_part(uint32_t acc, int c0, int count, float* part)
 {
-    const int quarter = (threadIdx.x / 32) % 4, lane = threadIdx.x & 31;
-    const int64_t j = t.feature + quarter * 32 + lane;
-    const bool in = j < a.n;
-    float bias = 0.f;
-    if (a.ep.bias && in) bias = to_f32<T>(static_cast<const T*>(a.ep.bias)[t.group * a.n + j]);
-    for (int c = 0; c < t.rows; c += 16) {
+    const int quarter = (threadIdx.x / 32) % 4, line = quarter * 32 + (threadIdx.x & 31);
+    for (int c = 0; c < count; c += 16) {
         uint32_t r[16];
-        tmem_load16(r, acc + ((uint32_t)quarter << 21) + c);
-        if (in) {
+        tmem_load16(r, acc + ((uint32_t)quarter << 21) + c0 + c);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (c + i < t.rows)
-                    finish<T>(a.ep, __uint_as_float(r[i]), S, bias, a.ep.bias != nullptr,
-                              (int64_t)(t.row + c + i) * a.n + j);
+        for (int i = 0; i < 16; ++i) part[(c + i) * kPartRow + line] = __uint_as_float(r[i]);
+    }
+}
+
+// Where one thread's 16 bytes of a chunk are.
+template <typename T> struct Item {
+    int token, lane;              // of the chunk; first feature of the tile
+    int64_t at;                   // element of y
+    int count;                    // features that exist
+    bool whole;
+    __device__ __forceinline__ Item(const TileArgs& a, const Tile& t, int c0, int i)
+    {
+        constexpr int kPer = 128 / Lanes<T>::kCount;
+        token = i / kPer;
+        lane = i % kPer * Lanes<T>::kCount;
+        const int64_t j = t.feature + lane;
+        count = (int)min((int64_t)Lanes<T>::kCount, a.n - j);
+        at = (int64_t)(t.row + c0 + token) * a.n + j;
+        whole = count == Lanes<T>::kCount && a.n % Lanes<T>::kCount == 0;
+    }
+};
+
+template <typename T, int N>
+__device__ __forceinline__ void load_bias(const TileArgs& a, const Tile& t, const Item<T>& it, float (&bias)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) bias[i] = 0.f;
+    if (a.ep.bias && it.count > 0) {
+        const int64_t j = t.group * a.n + t.feature + it.lane;
+        unpack16(load_lanes<T>(a.ep.bias, j, it.count, it.whole), bias);
+    }
+}
+
+// Tokens [0, t.rows) of a tile that one thread block summed.
+template <typename T, int kChunk>
+__device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part)
+{
+    constexpr int N = Lanes<T>::kCount, kPer = 128 / N, kItems = kChunk * kPer / 128;
+    const int tid = threadIdx.x & 127;
+    float bias[N];
+    load_bias<T>(a, t, Item<T>(a, t, 0, tid), bias);       // a thread keeps its features
+    for (int c0 = 0; c0 < t.rows; c0 += kChunk) {
+        const int rows = min(kChunk, t.rows - c0);
+        Extra<T> x[kItems];
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const Item<T> it(a, t, c0, k * 128 + tid);
+            if (it.token < rows && it.count > 0) x[k] = load_extra<T>(a.ep, it.at, it.count, it.whole);
         }
+        to_part(acc, c0, rows, part);
+        tile_bar();
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const Item<T> it(a, t, c0, k * 128 + tid);
+            if (it.token >= rows || it.count <= 0) continue;
+            float z[N];
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(part + it.token * kPartRow + it.lane + i);
+                z[i] = f.x * S;
+                z[i + 1] = f.y * S;
+                z[i + 2] = f.z * S;
+                z[i + 3] = f.w * S;
+            }
+            finish<T>(a.ep, z, bias, x[k], it.at, it.count, it.whole);
+        }
+        tile_bar();
     }
 }
 
 // The same where a cluster split the steps: every thread block leaves its
-// partial sums in shared memory, and each finishes its share of the tokens,
+// partial sums in shared memory, and each finishes its share of the outputs,
 // adding the partials in rank order (the result does not depend on timing).
 // `full`/`empty`: barriers of `split` arrivals, one from every thread block.
 template <typename T>
@@ -139,33 +204,45 @@ __device__ __forceinline__ bool write_tile_split(const TileArgs& a, const Tile& 
                                                  uint32_t full, uint32_t empty, uint32_t parity, uint32_t rank,
                                                  volatile int* dead, uint32_t acc_empty)
 {
-    const int quarter = (threadIdx.x / 32) % 4, lane = threadIdx.x & 31, line = quarter * 32 + lane;
-    bool ok = mbar_wait(empty, parity ^ 1, dead);       // every peer has read the tile before
-    if (ok)
-        for (int c = 0; c < t.rows; c += 16) {
-            uint32_t r[16];
-            tmem_load16(r, acc + ((uint32_t)quarter << 21) + c);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) part[(c + i) * 128 + line] = __uint_as_float(r[i]);
-        }
+    constexpr int N = Lanes<T>::kCount, kPer = 128 / N;
+    const int tid = threadIdx.x & 127;
+    bool ok = mbar_wait(empty, parity ^ 1, dead);          // every peer has read the tile before
+    const int first = (int)rank * 128 + tid;
+    const Item<T> it0(a, t, 0, first);
+    Extra<T> x;
+    float bias[N];
+    load_bias<T>(a, t, it0, bias);
+    if (it0.token < t.rows && it0.count > 0) x = load_extra<T>(a.ep, it0.at, it0.count, it0.whole);
+    if (ok) to_part(acc, 0, t.rows, part);
     tc_fence_before();
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    if (line == 0) mbar_arrive(acc_empty);
-    if (line < a.split) mbar_arrive_peer(full, line);
+    tile_bar();
+    if (tid == 0) mbar_arrive(acc_empty);
+    if (tid < a.split) mbar_arrive_peer(full, tid);
     ok = mbar_wait(full, parity, dead) && ok;
-    const int64_t j = t.feature + line;
-    if (ok && j < a.n) {
-        float bias = 0.f;
-        if (a.ep.bias) bias = to_f32<T>(static_cast<const T*>(a.ep.bias)[t.group * a.n + j]);
-        for (int c = (int)rank; c < t.rows; c += a.split) {
-            const uint32_t at = smem_u32(part + c * 128 + line);
-            float sum = ld_peer_f32(at, 0);
-            for (int q = 1; q < a.split; ++q) sum += ld_peer_f32(at, q);
-            finish<T>(a.ep, sum, S, bias, a.ep.bias != nullptr, (int64_t)(t.row + c) * a.n + j);
+    for (int i = first; ok && i < t.rows * kPer; i += a.split * 128) {
+        const Item<T> it(a, t, 0, i);
+        if (it.count <= 0) continue;
+        if (i != first) x = load_extra<T>(a.ep, it.at, it.count, it.whole);
+        const uint32_t from = smem_u32(part + it.token * kPartRow + it.lane);
+        float z[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) z[k] = 0.f;
+        for (int q = 0; q < a.split; ++q) {
+#pragma unroll
+            for (int k = 0; k < N; k += 4) {
+                const float4 f = ld_peer_f32x4(from + 4 * k, q);
+                z[k] += f.x;
+                z[k + 1] += f.y;
+                z[k + 2] += f.z;
+                z[k + 3] += f.w;
+            }
         }
+#pragma unroll
+        for (int k = 0; k < N; ++k) z[k] *= S;
+        finish<T>(a.ep, z, bias, x, it.at, it.count, it.whole);
     }
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    if (line < a.split) mbar_arrive_peer(empty, line);
+    tile_bar();
+    if (tid < a.split) mbar_arrive_peer(empty, tid);
     return ok;
 }
 

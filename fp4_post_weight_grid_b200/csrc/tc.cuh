@@ -46,41 +46,31 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ uint64_t global_ns()
-{
-    uint64_t t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
-}
-
-constexpr uint64_t kWaitNs = 2000000000ull;     // longest wait: two seconds
+constexpr long long kWaitClocks = 1ll << 32;    // longest wait: about two seconds of SM clocks
 
 // True once the barrier's phase `parity` has completed; false if the thread
-// block is dead or the wait ran out (which makes it dead).
-static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* dead)
+// block is dead or the wait ran out (which makes it dead).  Time is the SM's
+// own clock.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead)
 {
-    const uint64_t t0 = global_ns();
+    if (mbar_try(bar, parity)) return true;
+    const long long t0 = clock64();
     for (;;) {
-        for (int i = 0; i < 16; ++i)
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
             if (mbar_try(bar, parity)) return true;
         if (*dead) return false;
-        if (global_ns() - t0 > kWaitNs) {
+        if (clock64() - t0 > kWaitClocks) {
             *dead = 1;
             return false;
         }
     }
 }
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead)
-{
-    for (int i = 0; i < 4; ++i)
-        if (mbar_try(bar, parity)) return true;
-    return mbar_wait_slow(bar, parity, dead);
-}
 // For the end of a dead thread block: the wait for what it has in flight.
-static __device__ __noinline__ void mbar_drain(uint32_t bar, uint32_t parity)
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity)
 {
-    const uint64_t t0 = global_ns();
-    while (!mbar_try(bar, parity) && global_ns() - t0 < kWaitNs / 16) {
+    const long long t0 = clock64();
+    while (!mbar_try(bar, parity) && clock64() - t0 < kWaitClocks / 16) {
     }
 }
 
@@ -95,14 +85,14 @@ __device__ __forceinline__ void cluster_sync_all()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ld_peer_f32(uint32_t addr, uint32_t rank)
+__device__ __forceinline__ float4 ld_peer_f32x4(uint32_t addr, uint32_t rank)
 {
-    float v;
+    float4 v;
     asm volatile(
         "{\n\t.reg .b32 a;\n\t"
-        "mapa.shared::cluster.u32 a, %1, %2;\n\t"
-        "ld.shared::cluster.f32 %0, [a];\n\t}"
-        : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank) : "memory");
     return v;
 }
 
