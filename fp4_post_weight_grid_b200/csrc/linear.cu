@@ -22,22 +22,23 @@ namespace {
 
 constexpr int kStepCols = 256;             // columns of a step of W: 128 bytes of codes
 constexpr int kSubCols = 64;               // columns of a step of x and of decoded W
-constexpr int kASteps = 4;                 // decoded steps in tensor memory
 constexpr int kACols = kSubCols / 2;       // columns of tensor memory per decoded step
 
 template <int BN> struct Config {
     static constexpr int kW = 128 * 128, kWStage = kW + 4 * 512, kX = BN * 128;
-    static constexpr int kWStages = BN >= 256 ? 2 : BN >= 128 ? 5 : BN >= 64 ? 7 : 4;
-    static constexpr int kXStages = BN >= 256 ? 5 : BN >= 64 ? 6 : BN >= 32 ? 4 : 8;
+    static constexpr int kWStages = BN >= 256 ? 2 : BN >= 128 ? 5 : BN >= 64 ? 7 : 8;
+    static constexpr int kXStages = BN >= 256 ? 5 : BN >= 128 ? 6 : BN >= 64 ? 4 : 8;
     static constexpr int kAccs = BN <= 128 ? 2 : 1;
-    static constexpr int kDq = BN <= 32 ? 1 : 2;                    // groups of four decoding warps
+    static constexpr int kDq = BN <= 64 ? 4 : 2;                    // groups of four decoding warps
     static constexpr int kThreads = (4 + 4 * kDq + 4) * 32;
+    static constexpr int kADepth = 2;                               // decoded steps in tensor memory, per group
+    static constexpr int kASteps = kDq * kADepth;
     static constexpr int kUsed = kAccs * BN + kASteps * kACols;
     static constexpr int kCols = kUsed <= 256 ? 256 : 512;
     static constexpr bool kSplits = BN <= 64;
     static constexpr int kPart = (kSplits ? BN : 32) * kPartRow * 4;        // sums on their way to y
     static constexpr int kSmem = kWStages * kWStage + kXStages * kX + kPart + 1024;
-    static constexpr int kResident = BN <= 32 ? 2 : 1;
+    static constexpr int kResident = 1;
     static_assert(kUsed <= 512 && kCols * kResident <= 512, "tensor memory");
     static_assert(kSmem <= 222 * 1024 && kWStage % 1024 == 0 && kX % 1024 == 0, "shared memory");
 };
@@ -119,7 +120,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
 {
     using C = Config<BN>;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t bars[2 * (C::kWStages + C::kXStages + kASteps + C::kAccs) + 3];
+    __shared__ __align__(8) uint64_t bars[2 * (C::kWStages + C::kXStages + C::kASteps + C::kAccs) + 3];
     __shared__ int before[FP4Q_PRODUCT_GROUPS_MAX + 1];
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_word, good_offsets;
@@ -130,8 +131,8 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     uint8_t* x_ring = w_ring + C::kWStages * C::kWStage;
     float* part = reinterpret_cast<float*>(x_ring + C::kXStages * C::kX);
     const uint32_t w_full = smem_u32(bars), w_empty = w_full + 8 * C::kWStages, x_full = w_empty + 8 * C::kWStages,
-                   x_empty = x_full + 8 * C::kXStages, a_full = x_empty + 8 * C::kXStages, a_empty = a_full + 8 * kASteps,
-                   acc_full = a_empty + 8 * kASteps, acc_empty = acc_full + 8 * C::kAccs,
+                   x_empty = x_full + 8 * C::kXStages, a_full = x_empty + 8 * C::kXStages, a_empty = a_full + 8 * C::kASteps,
+                   acc_full = a_empty + 8 * C::kASteps, acc_empty = acc_full + 8 * C::kAccs,
                    part_full = acc_empty + 8 * C::kAccs, part_empty = part_full + 8, drain = part_empty + 8;
     const uint32_t rank = a.split > 1 ? cluster_rank() : 0;
 
@@ -146,7 +147,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 mbar_init(x_full + 8 * i, 1);
                 mbar_init(x_empty + 8 * i, 1);
             }
-            for (int i = 0; i < kASteps; ++i) {
+            for (int i = 0; i < C::kASteps; ++i) {
                 mbar_init(a_full + 8 * i, 4);
                 mbar_init(a_empty + 8 * i, 1);
             }
@@ -225,7 +226,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            uint32_t j = 0, n = 0;
+            uint32_t j = 0, n = 0, used[C::kDq] = {};
             bool ok = true;
             for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ++n) {
                 const Tile tl = tile_at<BN>(a, before, t);
@@ -233,19 +234,27 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 const uint32_t ac = n % C::kAccs, acc = tmem + ac * BN;
                 if (!(ok = mbar_wait(acc_empty + 8 * ac, (n / C::kAccs & 1) ^ 1, dead))) break;
                 tc_fence_after();
-                const int total = (min(a.k, k1 * kStepCols) - k0 * kStepCols + kSubCols - 1) / kSubCols;
-                for (int i = 0; i < total; ++i, ++j) {
-                    const uint32_t as = j % kASteps, xs = j % C::kXStages;
-                    if (!(ok = mbar_wait(x_full + 8 * xs, j / C::kXStages & 1, dead) &&
-                               mbar_wait(a_full + 8 * as, j / kASteps & 1, dead)))
-                        break;
-                    tc_fence_after();
+                for (int k = k0; ok && k < k1; ++k) {
+                    const int count = subs(k);
 #pragma unroll
-                    for (int c = 0; c < kSubCols / 16; ++c)
-                        tc_mma_bf16(acc, a_tmem + as * kACols + c * 8,
-                                    desc_k128(smem_u32(x_ring) + xs * C::kX + c * 32), idesc, i > 0 || c > 0);
-                    tc_commit(a_empty + 8 * as);
-                    tc_commit(x_empty + 8 * xs);
+                    for (int i = 0; i < kStepCols / kSubCols; ++i) {
+                        if (!ok || i >= count) break;
+                        uint32_t& u = used[i % C::kDq];
+                        const uint32_t as = i % C::kDq * C::kADepth + u % C::kADepth, xs = j % C::kXStages;
+                        if (!(ok = mbar_wait(x_full + 8 * xs, j / C::kXStages & 1, dead) &&
+                                   mbar_wait(a_full + 8 * as, u / C::kADepth & 1, dead)))
+                            break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < kSubCols / 16; ++c)
+                            tc_mma_bf16(acc, a_tmem + as * kACols + c * 8,
+                                        desc_k128(smem_u32(x_ring) + xs * C::kX + c * 32), idesc,
+                                        k > k0 || i > 0 || c > 0);
+                        tc_commit(a_empty + 8 * as);
+                        tc_commit(x_empty + 8 * xs);
+                        ++u;
+                        ++j;
+                    }
                 }
                 tc_commit(acc_full + 8 * ac);
             }
@@ -256,7 +265,9 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         }
     } else if (warp >= 4 && warp < 4 + 4 * C::kDq) {
         const int group = (warp - 4) / 4, quarter = warp % 4, row = quarter * 32 + lane;
-        uint32_t it = 0, j = 0;
+        // A group decodes into stages of its own: where a step has fewer
+        // sub-steps than there are groups, they run on at different paces.
+        uint32_t it = 0, used = 0;
         bool ok = true;
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
             for (int k = k0; ok && k < k1; ++k, ++it) {
@@ -265,8 +276,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 const uint8_t* codes = w_ring + s * C::kWStage + row * 128;
                 const uint8_t* scales = w_ring + s * C::kWStage + C::kW + lane * 16 + quarter * 4;
                 const int n = subs(k);
-                for (int i = 0; i < n; ++i, ++j) {
-                    if (C::kDq > 1 && i % C::kDq != group) continue;
+                for (int i = group; i < n; i += C::kDq, ++used) {
                     const uint4 c0 = *reinterpret_cast<const uint4*>(codes + ((2 * i) ^ (row & 7)) * 16);
                     const uint4 c1 = *reinterpret_cast<const uint4*>(codes + ((2 * i + 1) ^ (row & 7)) * 16);
                     const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + (MX ? i / 2 : i) * 512);
@@ -292,8 +302,8 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                             decode8(w[2 * h + 1], f, r + 8 * h + 4);
                         }
                     }
-                    const uint32_t as = j % kASteps;
-                    if (!(ok = mbar_wait(a_empty + 8 * as, (j / kASteps & 1) ^ 1, dead))) break;
+                    const uint32_t as = group * C::kADepth + used % C::kADepth;
+                    if (!(ok = mbar_wait(a_empty + 8 * as, (used / C::kADepth & 1) ^ 1, dead))) break;
                     tc_fence_after();
                     tmem_store32(a_tmem + as * kACols + ((uint32_t)quarter << 21), r);
                     tc_fence_before();

@@ -58,11 +58,27 @@ __device__ __forceinline__ uint4 pack16(const float (&v)[8])
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The GELUs in the forms without cancellation for negative z: Phi(z) =
-// erfc(-z/sqrt 2)/2, and 1 + tanh(u) = 2/(1 + exp(-2u)).  The hardware
-// exponential and division (a few units in the last place of binary32; the
-// exponential's grow with its argument where the result vanishes) keep the
-// activation below the cost of the product.  A NaN stays a NaN in every one.
+// z * Phi(z) from the rational approximation of erfc by Abramowitz and Stegun,
+// "Handbook of Mathematical Functions", 7.1.26 (absolute error 1.5e-7, a step
+// of binary32 near 1): with x = |z|/sqrt 2, t = 1/(1 + p x), Phi(-|z|) =
+// (a1 t + .. + a5 t^5) exp(-x^2) / 2, so that neither sign of z cancels.
+__device__ __forceinline__ float gelu(float z)
+{
+    const float x = fabsf(z) * 0.70710678f, t = __fdividef(1.f, 1.f + 0.3275911f * x);
+    float p = 1.061405429f;
+    p = p * t - 1.453152027f;
+    p = p * t + 1.421413741f;
+    p = p * t - 0.284496736f;
+    p = p * t + 0.254829592f;
+    const float phi = 0.5f * p * t * __expf(-x * x);
+    return z < 0.f ? z * phi : phi == 0.f ? z : z - z * phi;       // z = +inf stays +inf
+}
+
+// The tanh GELU as z / (1 + exp(-2u)), as 1 + tanh(u) = 2/(1 + exp(-2u)) and
+// this form does not cancel.  The hardware exponential and division (a few
+// units in the last place of binary32; the exponential's grow with its
+// argument where the result vanishes) keep the activation below the cost of
+// the product.  A NaN stays a NaN in every one.
 template <int N> __device__ __forceinline__ void activate(float (&z)[N], int act)
 {
     if (act == FP4Q_ACT_SILU) {
@@ -74,46 +90,30 @@ template <int N> __device__ __forceinline__ void activate(float (&z)[N], int act
             z[i] = __fdividef(z[i], 1.f + __expf(-1.59576912f * (z[i] + 0.044715f * z[i] * z[i] * z[i])));
     } else if (act == FP4Q_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) z[i] = 0.5f * z[i] * erfcf(z[i] * -0.70710678f);
+        for (int i = 0; i < N; ++i) z[i] = gelu(z[i]);
     } else if (act == FP4Q_ACT_RELU) {
 #pragma unroll
         for (int i = 0; i < N; ++i) z[i] = z[i] < 0.f ? 0.f : z[i];
     }
 }
 
-// What the 16 bytes of y at element `at` need from mul and residual, loaded
-// ahead of their use.  y may be either of them: an element is read by the
-// thread that then writes it.  `whole`: all of them exist and are aligned.
-template <typename T> struct Extra {
+// mul and residual of 16 bytes of y, loaded ahead of their use.  y may be
+// either of them: an element is read by the thread that then writes it.
+struct Extra {
     uint4 mul, residual;
 };
-template <typename T> __device__ __forceinline__ uint4 load_lanes(const void* p, int64_t at, int count, bool whole)
+template <typename T> __device__ __forceinline__ Extra load_extra(const EpilogueArgs& e, int64_t at)
 {
-    const T* q = static_cast<const T*>(p) + at;
-    if (whole) return *reinterpret_cast<const uint4*>(q);
-    float v[Lanes<T>::kCount];
-#pragma unroll
-    for (int i = 0; i < Lanes<T>::kCount; ++i) v[i] = i < count ? to_f32<T>(q[i]) : 0.f;
-    return pack16(v);
-}
-template <typename T>
-__device__ __forceinline__ Extra<T> load_extra(const EpilogueArgs& e, int64_t at, int count, bool whole)
-{
-    Extra<T> x;
-    if (e.mul) x.mul = load_lanes<T>(e.mul, at, count, whole);
-    if (e.residual) x.residual = load_lanes<T>(e.residual, at, count, whole);
+    Extra x;
+    if (e.mul) x.mul = *reinterpret_cast<const uint4*>(static_cast<const T*>(e.mul) + at);
+    if (e.residual) x.residual = *reinterpret_cast<const uint4*>(static_cast<const T*>(e.residual) + at);
     return x;
 }
-// bias: of the same elements, zeros where there is none (adding zero changes
-// no value but the sign of a zero).
+// The 16 bytes of y from sums that have their bias and activation.
 template <typename T, int N>
-__device__ __forceinline__ void finish(const EpilogueArgs& e, float (&z)[N], const float (&bias)[N], const Extra<T>& x,
-                                       int64_t at, int count, bool whole)
+__device__ __forceinline__ void finish(const EpilogueArgs& e, float (&z)[N], const Extra& x, int64_t at)
 {
     static_assert(N == Lanes<T>::kCount, "16 bytes");
-#pragma unroll
-    for (int i = 0; i < N; ++i) z[i] += bias[i];
-    if (e.act != FP4Q_ACT_NONE) activate(z, e.act);
     float v[N];
     if (e.mul) {
         unpack16(x.mul, v);
@@ -125,14 +125,14 @@ __device__ __forceinline__ void finish(const EpilogueArgs& e, float (&z)[N], con
 #pragma unroll
         for (int i = 0; i < N; ++i) z[i] += v[i];
     }
-    T* q = static_cast<T*>(e.y) + at;
-    if (whole) {
-        *reinterpret_cast<uint4*>(q) = pack16(z);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (i < count) q[i] = from_f32<T>(z[i]);
-    }
+    *reinterpret_cast<uint4*>(static_cast<T*>(e.y) + at) = pack16(z);
+}
+// One element, for rows that do not start on 16-byte boundaries.
+template <typename T> __device__ __forceinline__ void finish_one(const EpilogueArgs& e, float z, int64_t at)
+{
+    if (e.mul) z *= to_f32<T>(static_cast<const T*>(e.mul)[at]);
+    if (e.residual) z += to_f32<T>(static_cast<const T*>(e.residual)[at]);
+    static_cast<T*>(e.y)[at] = from_f32<T>(z);
 }
 
 }  // namespace fp4q

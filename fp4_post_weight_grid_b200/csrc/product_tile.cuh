@@ -118,44 +118,39 @@ template <typename T, int BN> struct Chunk {
 
 __device__ __forceinline__ void tile_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-__device__ __forceinline__ void to_part(uint32_t acc, int c0, int count, float* part)
+// Columns [c0, c0 + count) of the accumulator; S, bias and act are applied
+// on the way where `last` (the sums are complete).
+template <bool last>
+__device__ __forceinline__ void to_part(uint32_t acc, int c0, int count, float* part, float S, float bias, int act)
 {
     const int quarter = (threadIdx.x / 32) % 4, line = quarter * 32 + (threadIdx.x & 31);
+#pragma unroll 1
     for (int c = 0; c < count; c += 16) {
         uint32_t r[16];
         tmem_load16(r, acc + ((uint32_t)quarter << 21) + c0 + c);
+        float z[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) part[(c + i) * kPartRow + line] = __uint_as_float(r[i]);
+        for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(r[i]);
+        if (last) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[i] = z[i] * S + bias;
+            activate(z, act);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) part[(c + i) * kPartRow + line] = z[i];
     }
 }
 
-// Where one thread's 16 bytes of a chunk are.
-template <typename T> struct Item {
-    int token, lane;              // of the chunk; first feature of the tile
-    int64_t at;                   // element of y
-    int count;                    // features that exist
-    bool whole;
-    __device__ __forceinline__ Item(const TileArgs& a, const Tile& t, int c0, int i)
-    {
-        constexpr int kPer = 128 / Lanes<T>::kCount;
-        token = i / kPer;
-        lane = i % kPer * Lanes<T>::kCount;
-        const int64_t j = t.feature + lane;
-        count = (int)min((int64_t)Lanes<T>::kCount, a.n - j);
-        at = (int64_t)(t.row + c0 + token) * a.n + j;
-        whole = count == Lanes<T>::kCount && a.n % Lanes<T>::kCount == 0;
-    }
-};
-
-template <typename T, int N>
-__device__ __forceinline__ void load_bias(const TileArgs& a, const Tile& t, const Item<T>& it, float (&bias)[N])
+// Whether rows of y consist of whole 16-byte pieces.
+template <typename T> __device__ __forceinline__ bool whole_rows(const TileArgs& a)
 {
-#pragma unroll
-    for (int i = 0; i < N; ++i) bias[i] = 0.f;
-    if (a.ep.bias && it.count > 0) {
-        const int64_t j = t.group * a.n + t.feature + it.lane;
-        unpack16(load_lanes<T>(a.ep.bias, j, it.count, it.whole), bias);
-    }
+    return a.n % Lanes<T>::kCount == 0;
+}
+
+template <typename T> __device__ __forceinline__ float bias_of(const TileArgs& a, const Tile& t, int line)
+{
+    const int64_t j = t.feature + line;
+    return a.ep.bias && j < a.n ? to_f32<T>(static_cast<const T*>(a.ep.bias)[t.group * a.n + j]) : 0.f;
 }
 
 // Tokens [0, t.rows) of a tile that one thread block summed.
@@ -163,33 +158,41 @@ template <typename T, int kChunk>
 __device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part)
 {
     constexpr int N = Lanes<T>::kCount, kPer = 128 / N, kItems = kChunk * kPer / 128;
-    const int tid = threadIdx.x & 127;
-    float bias[N];
-    load_bias<T>(a, t, Item<T>(a, t, 0, tid), bias);       // a thread keeps its features
+    const int tid = threadIdx.x & 127, line = (threadIdx.x / 32) % 4 * 32 + (threadIdx.x & 31);
+    const float bias = bias_of<T>(a, t, line);
+    const bool whole = whole_rows<T>(a);
+    const int lane = tid % kPer * N, token0 = tid / kPer;             // a thread keeps its features
+    const bool in = whole && t.feature + lane < a.n;
+    const int64_t at0 = (int64_t)(t.row + token0) * a.n + t.feature + lane, step = (int64_t)(128 / kPer) * a.n;
+#pragma unroll 1
     for (int c0 = 0; c0 < t.rows; c0 += kChunk) {
         const int rows = min(kChunk, t.rows - c0);
-        Extra<T> x[kItems];
+        const int64_t at = at0 + (int64_t)c0 * a.n;
+        Extra x[kItems];
 #pragma unroll
-        for (int k = 0; k < kItems; ++k) {
-            const Item<T> it(a, t, c0, k * 128 + tid);
-            if (it.token < rows && it.count > 0) x[k] = load_extra<T>(a.ep, it.at, it.count, it.whole);
-        }
-        to_part(acc, c0, rows, part);
+        for (int k = 0; k < kItems; ++k)
+            if (in && token0 + k * (128 / kPer) < rows) x[k] = load_extra<T>(a.ep, at + k * step);
+        to_part<true>(acc, c0, rows, part, S, bias, a.ep.act);
         tile_bar();
+        if (whole) {
 #pragma unroll
-        for (int k = 0; k < kItems; ++k) {
-            const Item<T> it(a, t, c0, k * 128 + tid);
-            if (it.token >= rows || it.count <= 0) continue;
-            float z[N];
+            for (int k = 0; k < kItems; ++k) {
+                const int token = token0 + k * (128 / kPer);
+                if (!in || token >= rows) continue;
+                float z[N];
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(part + it.token * kPartRow + it.lane + i);
-                z[i] = f.x * S;
-                z[i + 1] = f.y * S;
-                z[i + 2] = f.z * S;
-                z[i + 3] = f.w * S;
+                for (int i = 0; i < N; i += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(part + token * kPartRow + lane + i);
+                    z[i] = f.x;
+                    z[i + 1] = f.y;
+                    z[i + 2] = f.z;
+                    z[i + 3] = f.w;
+                }
+                finish<T>(a.ep, z, x[k], at + k * step);
             }
-            finish<T>(a.ep, z, bias, x[k], it.at, it.count, it.whole);
+        } else if (t.feature + line < a.n) {
+            for (int c = 0; c < rows; ++c)
+                finish_one<T>(a.ep, part[c * kPartRow + line], (int64_t)(t.row + c0 + c) * a.n + t.feature + line);
         }
         tile_bar();
     }
@@ -207,39 +210,60 @@ __device__ __forceinline__ bool write_tile_split(const TileArgs& a, const Tile& 
     constexpr int N = Lanes<T>::kCount, kPer = 128 / N;
     const int tid = threadIdx.x & 127;
     bool ok = mbar_wait(empty, parity ^ 1, dead);          // every peer has read the tile before
-    const int first = (int)rank * 128 + tid;
-    const Item<T> it0(a, t, 0, first);
-    Extra<T> x;
-    float bias[N];
-    load_bias<T>(a, t, it0, bias);
-    if (it0.token < t.rows && it0.count > 0) x = load_extra<T>(a.ep, it0.at, it0.count, it0.whole);
-    if (ok) to_part(acc, 0, t.rows, part);
+    if (ok) to_part<false>(acc, 0, t.rows, part, 0.f, 0.f, 0);
     tc_fence_before();
     tile_bar();
     if (tid == 0) mbar_arrive(acc_empty);
     if (tid < a.split) mbar_arrive_peer(full, tid);
+    const bool whole = whole_rows<T>(a);
+    const int lane = tid % kPer * N;                       // a thread keeps its features
+    const bool in = whole && t.feature + lane < a.n;
+    int token = (int)rank * (128 / kPer) + tid / kPer;
+    int64_t at = (int64_t)(t.row + token) * a.n + t.feature + lane;
+    Extra x;
+    float bias[N];
+    if (in && token < t.rows) {
+        x = load_extra<T>(a.ep, at);
+#pragma unroll
+        for (int i = 0; i < N; ++i) bias[i] = bias_of<T>(a, t, lane + i);
+    }
     ok = mbar_wait(full, parity, dead) && ok;
-    for (int i = first; ok && i < t.rows * kPer; i += a.split * 128) {
-        const Item<T> it(a, t, 0, i);
-        if (it.count <= 0) continue;
-        if (i != first) x = load_extra<T>(a.ep, it.at, it.count, it.whole);
-        const uint32_t from = smem_u32(part + it.token * kPartRow + it.lane);
-        float z[N];
+    if (whole) {
+#pragma unroll 1
+        while (ok && in && token < t.rows) {
+            const uint32_t from = smem_u32(part + token * kPartRow + lane);
+            float z[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k) z[k] = 0.f;
-        for (int q = 0; q < a.split; ++q) {
+            for (int k = 0; k < N; ++k) z[k] = 0.f;
+#pragma unroll 2
+            for (int q = 0; q < a.split; ++q) {
 #pragma unroll
-            for (int k = 0; k < N; k += 4) {
-                const float4 f = ld_peer_f32x4(from + 4 * k, q);
-                z[k] += f.x;
-                z[k + 1] += f.y;
-                z[k + 2] += f.z;
-                z[k + 3] += f.w;
+                for (int k = 0; k < N; k += 4) {
+                    const float4 f = ld_peer_f32x4(from + 4 * k, q);
+                    z[k] += f.x;
+                    z[k + 1] += f.y;
+                    z[k + 2] += f.z;
+                    z[k + 3] += f.w;
+                }
             }
-        }
 #pragma unroll
-        for (int k = 0; k < N; ++k) z[k] *= S;
-        finish<T>(a.ep, z, bias, x, it.at, it.count, it.whole);
+            for (int k = 0; k < N; ++k) z[k] = z[k] * S + bias[k];
+            activate(z, a.ep.act);
+            finish<T>(a.ep, z, x, at);
+            token += a.split * (128 / kPer);
+            at += (int64_t)a.split * (128 / kPer) * a.n;
+            if (token < t.rows) x = load_extra<T>(a.ep, at);
+        }
+    } else if (ok && t.feature + tid < a.n) {
+        const float b = bias_of<T>(a, t, tid);
+        for (int c = (int)rank; c < t.rows; c += a.split) {
+            const uint32_t from = smem_u32(part + c * kPartRow + tid);
+            float z[1] = {0.f};
+            for (int q = 0; q < a.split; ++q) z[0] += ld_peer_f32(from, q);
+            z[0] = z[0] * S + b;
+            activate(z, a.ep.act);
+            finish_one<T>(a.ep, z[0], (int64_t)(t.row + c) * a.n + t.feature + tid);
+        }
     }
     tile_bar();
     if (tid < a.split) mbar_arrive_peer(empty, tid);

@@ -85,6 +85,16 @@ __device__ __forceinline__ void cluster_sync_all()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ float ld_peer_f32(uint32_t addr, uint32_t rank)
+{
+    float v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %1, %2;\n\t"
+        "ld.shared::cluster.f32 %0, [a];\n\t}"
+        : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+    return v;
+}
 __device__ __forceinline__ float4 ld_peer_f32x4(uint32_t addr, uint32_t rank)
 {
     float4 v;
