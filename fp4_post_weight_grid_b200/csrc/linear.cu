@@ -126,7 +126,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     __shared__ int dead_word, good_offsets;
     volatile int* dead = &dead_word;
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
     uint8_t* w_ring = raw + (1024 - smem_u32(raw) % 1024) % 1024;
     uint8_t* x_ring = w_ring + C::kWStages * C::kWStage;
     float* part = reinterpret_cast<float*>(x_ring + C::kXStages * C::kX);
@@ -183,111 +183,112 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     auto subs = [&](int k) { return min(kStepCols / kSubCols, (a.k - k * kStepCols + kSubCols - 1) / kSubCols); };
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-                const Tile tl = tile_at<BN>(a, before, t);
-                const int wrow = (int)(tl.group * a.n) + tl.feature;
-                const uint8_t* ws = a.w_scales + tl.group * a.w_scale_stride +
-                                    (int64_t)(tl.feature / 128) * a.w_col_tiles * 512;
-                for (int k = k0; k < k1; ++k, ++it) {
-                    const uint32_t s = it % C::kWStages;
-                    if (!(ok = mbar_wait(w_empty + 8 * s, (it / C::kWStages & 1) ^ 1, dead))) break;
-                    const uint32_t at = smem_u32(w_ring) + s * C::kWStage, bar = w_full + 8 * s;
-                    const int c0 = k * (kStepCols / kScaleTile);
-                    const uint32_t sb = (uint32_t)min(kStepCols / kScaleTile, a.w_col_tiles - c0) * 512;
+        Ring<C::kWStages> w;
+        bool ok = true;
+        for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+            const Tile tl = tile_at<BN>(a, before, t);
+            const int wrow = (int)(tl.group * a.n) + tl.feature;
+            const uint8_t* ws = a.w_scales + tl.group * a.w_scale_stride +
+                                (int64_t)(tl.feature / 128) * a.w_col_tiles * 512;
+            for (int k = k0; k < k1; ++k, w.next()) {
+                if (!(ok = mbar_wait(w_empty + 8 * w.stage, w.parity ^ 1, dead))) break;
+                const uint32_t at = smem_u32(w_ring) + w.stage * C::kWStage, bar = w_full + 8 * w.stage;
+                const int c0 = k * (kStepCols / kScaleTile);
+                const uint32_t sb = (uint32_t)min(kStepCols / kScaleTile, a.w_col_tiles - c0) * 512;
+                if (elect_one()) {
                     mbar_expect(bar, C::kW + sb);
                     tma_load(at, &w_map, k * (kStepCols / 2), wrow, bar);
                     bulk_load(at + C::kW, ws + (int64_t)c0 * 512, sb, bar);
                 }
+                __syncwarp();
             }
-            if (*dead)                                     // copies in flight end before the block does
-                for (uint32_t i = it < C::kWStages ? 0 : it - C::kWStages; i < it; ++i)
-                    mbar_drain(w_full + 8 * (i % C::kWStages), i / C::kWStages & 1);
         }
+        drain_ring(w, w_full, dead);
     } else if (warp == 3) {
-        if (lane == 0) {
-            uint32_t j = 0;
-            bool ok = true;
-            for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-                const Tile tl = tile_at<BN>(a, before, t);
-                const int c1 = min(a.k, k1 * kStepCols);
-                for (int c = k0 * kStepCols; c < c1; c += kSubCols, ++j) {
-                    const uint32_t s = j % C::kXStages;
-                    if (!(ok = mbar_wait(x_empty + 8 * s, (j / C::kXStages & 1) ^ 1, dead))) break;
-                    mbar_expect(x_full + 8 * s, C::kX);
-                    tma_load(smem_u32(x_ring) + s * C::kX, &x_map, c * 2, tl.row, x_full + 8 * s);
+        Ring<C::kXStages> x;
+        bool ok = true;
+        for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+            const Tile tl = tile_at<BN>(a, before, t);
+            const int c1 = min(a.k, k1 * kStepCols);
+            for (int c = k0 * kStepCols; c < c1; c += kSubCols, x.next()) {
+                if (!(ok = mbar_wait(x_empty + 8 * x.stage, x.parity ^ 1, dead))) break;
+                const uint32_t bar = x_full + 8 * x.stage;
+                if (elect_one()) {
+                    mbar_expect(bar, C::kX);
+                    tma_load(smem_u32(x_ring) + x.stage * C::kX, &x_map, c * 2, tl.row, bar);
                 }
+                __syncwarp();
             }
-            if (*dead)
-                for (uint32_t i = j < C::kXStages ? 0 : j - C::kXStages; i < j; ++i)
-                    mbar_drain(x_full + 8 * (i % C::kXStages), i / C::kXStages & 1);
         }
+        drain_ring(x, x_full, dead);
     } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t j = 0, n = 0, used[C::kDq] = {};
-            bool ok = true;
-            for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ++n) {
-                const Tile tl = tile_at<BN>(a, before, t);
-                const uint32_t idesc = idesc_bf16(min(BN, (tl.rows + 15) / 16 * 16));
-                const uint32_t ac = n % C::kAccs, acc = tmem + ac * BN;
-                if (!(ok = mbar_wait(acc_empty + 8 * ac, (n / C::kAccs & 1) ^ 1, dead))) break;
-                tc_fence_after();
-                for (int k = k0; ok && k < k1; ++k) {
-                    const int count = subs(k);
+        Ring<C::kXStages> x;
+        Ring<C::kADepth> dec[C::kDq];
+        Ring<C::kAccs> ac;
+        bool ok = true;
+        const uint64_t desc0 = desc_k128(smem_u32(x_ring));
+        for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next()) {
+            const Tile tl = tile_at<BN>(a, before, t);
+            const uint32_t idesc = idesc_bf16(min(BN, (tl.rows + 15) / 16 * 16));
+            const uint32_t acc = tmem + ac.stage * BN;
+            if (!(ok = mbar_wait(acc_empty + 8 * ac.stage, ac.parity ^ 1, dead))) break;
+            tc_fence_after();
+            for (int k = k0; ok && k < k1; ++k) {
+                const int count = subs(k);
 #pragma unroll
-                    for (int i = 0; i < kStepCols / kSubCols; ++i) {
-                        if (!ok || i >= count) break;
-                        uint32_t& u = used[i % C::kDq];
-                        const uint32_t as = i % C::kDq * C::kADepth + u % C::kADepth, xs = j % C::kXStages;
-                        if (!(ok = mbar_wait(x_full + 8 * xs, j / C::kXStages & 1, dead) &&
-                                   mbar_wait(a_full + 8 * as, u / C::kADepth & 1, dead)))
-                            break;
-                        tc_fence_after();
+                for (int i = 0; i < kStepCols / kSubCols; ++i) {
+                    if (!ok || i >= count) break;
+                    Ring<C::kADepth>& d = dec[i % C::kDq];
+                    const uint32_t as = i % C::kDq * C::kADepth + d.stage;
+                    if (!(ok = mbar_wait(x_full + 8 * x.stage, x.parity, dead) &&
+                               mbar_wait(a_full + 8 * as, d.parity, dead)))
+                        break;
+                    tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
                         for (int c = 0; c < kSubCols / 16; ++c)
-                            tc_mma_bf16(acc, a_tmem + as * kACols + c * 8,
-                                        desc_k128(smem_u32(x_ring) + xs * C::kX + c * 32), idesc,
-                                        k > k0 || i > 0 || c > 0);
+                            tc_mma_bf16(acc, a_tmem + as * kACols + c * 8, desc0 + x.stage * (C::kX >> 4) + c * 2,
+                                        idesc, k > k0 || i > 0 || c > 0);
                         tc_commit(a_empty + 8 * as);
-                        tc_commit(x_empty + 8 * xs);
-                        ++u;
-                        ++j;
+                        tc_commit(x_empty + 8 * x.stage);
                     }
+                    __syncwarp();
+                    d.next();
+                    x.next();
                 }
-                tc_commit(acc_full + 8 * ac);
             }
-            if (*dead) {
-                tc_commit(drain);
-                mbar_drain(drain, 0);
-            }
+            if (elect_one()) tc_commit(acc_full + 8 * ac.stage);
+            __syncwarp();
+        }
+        if (*dead) {
+            if (elect_one()) tc_commit(drain);
+            mbar_drain(drain, 0);
         }
     } else if (warp >= 4 && warp < 4 + 4 * C::kDq) {
         const int group = (warp - 4) / 4, quarter = warp % 4, row = quarter * 32 + lane;
         // A group decodes into stages of its own: where a step has fewer
         // sub-steps than there are groups, they run on at different paces.
-        uint32_t it = 0, used = 0;
+        Ring<C::kWStages> w;
+        Ring<C::kADepth> d;
         bool ok = true;
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-            for (int k = k0; ok && k < k1; ++k, ++it) {
-                const uint32_t s = it % C::kWStages;
-                if (!(ok = mbar_wait(w_full + 8 * s, it / C::kWStages & 1, dead))) break;
-                const uint8_t* codes = w_ring + s * C::kWStage + row * 128;
-                const uint8_t* scales = w_ring + s * C::kWStage + C::kW + lane * 16 + quarter * 4;
+            for (int k = k0; ok && k < k1; ++k, w.next()) {
+                if (!(ok = mbar_wait(w_full + 8 * w.stage, w.parity, dead))) break;
+                const uint8_t* codes = w_ring + w.stage * C::kWStage + row * 128;
+                const uint8_t* scales = w_ring + w.stage * C::kWStage + C::kW + lane * 16 + quarter * 4;
                 const int n = subs(k);
-                for (int i = group; i < n; i += C::kDq, ++used) {
+                for (int i = group; i < n; i += C::kDq, d.next()) {
                     const uint4 c0 = *reinterpret_cast<const uint4*>(codes + ((2 * i) ^ (row & 7)) * 16);
                     const uint4 c1 = *reinterpret_cast<const uint4*>(codes + ((2 * i + 1) ^ (row & 7)) * 16);
                     const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + (MX ? i / 2 : i) * 512);
-                    const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                    const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
                     uint32_t r[32];
                     if (MX) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t b = (sc >> (16 * (i & 1) + 8 * h)) & 255, f = mx_factor(b);
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) decode8(w[4 * h + q], f, r + 16 * h + 4 * q);
+                            for (int q = 0; q < 4; ++q) decode8(c[4 * h + q], f, r + 16 * h + 4 * q);
                             if (b > 130) {
                                 const uint32_t f2 = mx_rest(b);
 #pragma unroll
@@ -298,12 +299,12 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
                             const uint32_t f = nv_factor((sc >> (8 * h)) & 255);
-                            decode8(w[2 * h], f, r + 8 * h);
-                            decode8(w[2 * h + 1], f, r + 8 * h + 4);
+                            decode8(c[2 * h], f, r + 8 * h);
+                            decode8(c[2 * h + 1], f, r + 8 * h + 4);
                         }
                     }
-                    const uint32_t as = group * C::kADepth + used % C::kADepth;
-                    if (!(ok = mbar_wait(a_empty + 8 * as, (used / C::kADepth & 1) ^ 1, dead))) break;
+                    const uint32_t as = group * C::kADepth + d.stage;
+                    if (!(ok = mbar_wait(a_empty + 8 * as, d.parity ^ 1, dead))) break;
                     tc_fence_after();
                     tmem_store32(a_tmem + as * kACols + ((uint32_t)quarter << 21), r);
                     tc_fence_before();
@@ -311,26 +312,27 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                     if (lane == 0) mbar_arrive(a_full + 8 * as);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(w_empty + 8 * s);
+                if (lane == 0) mbar_arrive(w_empty + 8 * w.stage);
             }
         }
     } else if (warp >= 4 + 4 * C::kDq) {
-        uint32_t n = 0;
+        Ring<C::kAccs> ac;
+        uint32_t parity = 0;
         bool ok = true;
-        for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ++n) {
+        for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next(), parity ^= 1) {
             const Tile tl = tile_at<BN>(a, before, t);
-            const uint32_t ac = n % C::kAccs, acc = tmem + ac * BN;
+            const uint32_t acc = tmem + ac.stage * BN;
             const float S = MX ? 4.f : a.w_S[tl.group] * 128.f;        // the decoded weights are scaled down
-            ok = mbar_wait(acc_full + 8 * ac, n / C::kAccs & 1, dead);
+            ok = mbar_wait(acc_full + 8 * ac.stage, ac.parity, dead);
             tc_fence_after();
             if (C::kSplits && a.split > 1) {
-                ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, n & 1, rank, dead,
-                                         acc_empty + 8 * ac) && ok;
+                ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, parity, rank, dead,
+                                         acc_empty + 8 * ac.stage) && ok;
             } else {
                 if (ok) write_tile<T, Chunk<T, BN>::kTokens>(a, tl, acc, S, part);
                 tc_fence_before();
                 tile_bar();
-                if (warp % 4 == 0 && lane == 0) mbar_arrive(acc_empty + 8 * ac);
+                if (warp % 4 == 0 && lane == 0) mbar_arrive(acc_empty + 8 * ac.stage);
             }
         }
     }

@@ -56,7 +56,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     __shared__ int dead_word, good_offsets;
     volatile int* dead = &dead_word;
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
     uint8_t* ring = raw + (1024 - smem_u32(raw) % 1024) % 1024;
     float* part = reinterpret_cast<float*>(ring + C::kStages * C::kStage);
     const uint32_t ring0 = smem_u32(ring);
@@ -97,74 +97,78 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     const int64_t tiles = good_offsets ? (int64_t)before[a.groups] * a.n_tiles : 0;
     if (!good_offsets && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, FP4Q_FLAG_OFFSETS);
     const int64_t first_tile = blockIdx.x / a.split, tile_step = gridDim.x / a.split;
-    const int per_tile = MX ? 128 : 64;                    // columns of a scale tile
+    constexpr int per_tile = MX ? 128 : 64;                    // columns of a scale tile
     int k0, k1;
     split_steps(a, (int)rank, k0, k1);
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-                const Tile tl = tile_at<BN>(a, before, t);
-                const int wrow = (int)(tl.group * a.n) + tl.feature;
-                const uint8_t* ws = a.w_scales + tl.group * a.w_scale_stride +
-                                    (int64_t)(tl.feature / 128) * a.w_col_tiles * 512;
-                for (int k = k0; k < k1; ++k, ++it) {
-                    const uint32_t s = it % C::kStages;
-                    if (!(ok = mbar_wait(empty + 8 * s, (it / C::kStages & 1) ^ 1, dead))) break;
-                    const uint32_t at = ring0 + s * C::kStage, bar = full + 8 * s;
-                    const int c0 = k * (kStepCols / per_tile);
-                    const uint32_t sb = (uint32_t)min(kStepCols / per_tile, a.w_col_tiles - c0) * 512;
+        Ring<C::kStages> g;
+        bool ok = true;
+        for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+            const Tile tl = tile_at<BN>(a, before, t);
+            const int wrow = (int)(tl.group * a.n) + tl.feature;
+            const uint8_t* ws = a.w_scales + tl.group * a.w_scale_stride +
+                                (int64_t)(tl.feature / 128) * a.w_col_tiles * 512;
+            for (int k = k0; k < k1; ++k, g.next()) {
+                if (!(ok = mbar_wait(empty + 8 * g.stage, g.parity ^ 1, dead))) break;
+                const uint32_t at = ring0 + g.stage * C::kStage, bar = full + 8 * g.stage;
+                const int c0 = k * (kStepCols / per_tile);
+                const uint32_t sb = (uint32_t)min(kStepCols / per_tile, a.w_col_tiles - c0) * 512;
+                if (elect_one()) {
                     mbar_expect(bar, C::kW + C::kX + sb);
                     tma_load(at, &w_map, k * (kStepCols / 2), wrow, bar);
                     tma_load(at + C::kW, &x_map, k * (kStepCols / 2), tl.row, bar);
                     bulk_load(at + C::kW + C::kX, ws + (int64_t)c0 * 512, sb, bar);
                 }
+                __syncwarp();
             }
-            if (*dead)                                     // copies in flight end before the block does
-                for (uint32_t i = it < C::kStages ? 0 : it - C::kStages; i < it; ++i)
-                    mbar_drain(full + 8 * (i % C::kStages), i / C::kStages & 1);
         }
+        drain_ring(g, full, dead);
     } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t it = 0, n = 0;
-            bool ok = true;
-            for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ++n) {
-                const Tile tl = tile_at<BN>(a, before, t);
-                const uint32_t cols = min(BN, (tl.rows + 15) / 16 * 16);
-                const uint32_t ac = n % C::kAccs, acc = tmem + ac * BN;
-                if (!(ok = mbar_wait(acc_empty + 8 * ac, (n / C::kAccs & 1) ^ 1, dead))) break;
+        Ring<C::kStages> g;
+        Ring<C::kAccs> ac;
+        bool ok = true;
+        for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next()) {
+            const Tile tl = tile_at<BN>(a, before, t);
+            const uint32_t cols = min(BN, (tl.rows + 15) / 16 * 16);
+            const uint32_t acc = tmem + ac.stage * BN;
+            if (!(ok = mbar_wait(acc_empty + 8 * ac.stage, ac.parity ^ 1, dead))) break;
+            tc_fence_after();
+            for (int k = k0; k < k1; ++k, g.next()) {
+                if (!(ok = mbar_wait(full + 8 * g.stage, g.parity, dead))) break;
                 tc_fence_after();
-                for (int k = k0; k < k1; ++k, ++it) {
-                    const uint32_t s = it % C::kStages;
-                    if (!(ok = mbar_wait(full + 8 * s, it / C::kStages & 1, dead))) break;
-                    tc_fence_after();
-                    const uint32_t at = ring0 + s * C::kStage;
-                    const uint32_t sf = tmem + C::kAccs * BN + s * C::kScaleCols;
-                    const int parts = min(kStepCols / kMmaCols, (a.k - k * kStepCols + kMmaCols - 1) / kMmaCols);
-                    const int scale_tiles = MX ? (parts + 1) / 2 : parts;
-                    for (int i = 0; i < scale_tiles; ++i) {
-                        tc_copy_scales(sf + i * 4, desc_scales(at + C::kW + C::kX + i * 512));
+                const uint32_t at = ring0 + g.stage * C::kStage;
+                const uint32_t sf = tmem + C::kAccs * BN + g.stage * C::kScaleCols;
+                const int parts = min(kStepCols / kMmaCols, (a.k - k * kStepCols + kMmaCols - 1) / kMmaCols);
+                const uint64_t wd = desc_k128(at), xd = desc_k128(at + C::kW),
+                               sd = desc_scales(at + C::kW + C::kX);
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < kStepCols / per_tile; ++i) {
+                        if (i * (per_tile / kMmaCols) >= parts) break;
+                        tc_copy_scales(sf + i * 4, sd + i * (512 >> 4));
 #pragma unroll
                         for (int h = 0; h < C::kTokenTiles; ++h)
                             tc_copy_scales(sf + 16 + i * 4 * C::kTokenTiles + h * 4,
-                                           desc_scales(at + C::kW + C::kX + C::kWS + (i * C::kTokenTiles + h) * 512));
+                                           sd + ((C::kWS + (i * C::kTokenTiles + h) * 512) >> 4));
                     }
-                    for (int i = 0; i < parts; ++i) {
+#pragma unroll
+                    for (int i = 0; i < kStepCols / kMmaCols; ++i) {
+                        if (i >= parts) break;
                         const int st = MX ? i / 2 : i;
-                        tc_mma_fp4<MX>(acc, desc_k128(at + i * 32), desc_k128(at + C::kW + i * 32),
-                                       idesc_fp4(MX, cols, MX ? (i % 2) * 2 : 0), sf + st * 4,
-                                       sf + 16 + st * 4 * C::kTokenTiles, k > k0 || i > 0);
+                        tc_mma_fp4<MX>(acc, wd + i * 2, xd + i * 2, idesc_fp4(MX, cols, MX ? (i % 2) * 2 : 0),
+                                       sf + st * 4, sf + 16 + st * 4 * C::kTokenTiles, k > k0 || i > 0);
                     }
-                    tc_commit(empty + 8 * s);
+                    tc_commit(empty + 8 * g.stage);
                 }
-                tc_commit(acc_full + 8 * ac);
+                __syncwarp();
             }
-            if (*dead) {
-                tc_commit(drain);
-                mbar_drain(drain, 0);
-            }
+            if (elect_one()) tc_commit(acc_full + 8 * ac.stage);
+            __syncwarp();
+        }
+        if (*dead) {
+            if (elect_one()) tc_commit(drain);
+            mbar_drain(drain, 0);
         }
     } else if (warp < 4) {
         // Token scales: thread i of the 64 takes rows i, i + 64, ...; a row's
@@ -218,22 +222,23 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         if (lane == 0)
             for (uint32_t i = it < kLag ? 0 : it - kLag; i < it; ++i) mbar_arrive(full + 8 * (i % C::kStages));
     } else {
-        uint32_t n = 0;
+        Ring<C::kAccs> ac;
+        uint32_t parity = 0;
         bool ok = true;
-        for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ++n) {
+        for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next(), parity ^= 1) {
             const Tile tl = tile_at<BN>(a, before, t);
-            const uint32_t ac = n % C::kAccs, acc = tmem + ac * BN;
+            const uint32_t acc = tmem + ac.stage * BN;
             const float S = MX ? 1.f : a.w_S[tl.group] * *a.x_S;
-            ok = mbar_wait(acc_full + 8 * ac, n / C::kAccs & 1, dead);
+            ok = mbar_wait(acc_full + 8 * ac.stage, ac.parity, dead);
             tc_fence_after();
             if (C::kSplits && a.split > 1) {
-                ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, n & 1, rank, dead,
-                                         acc_empty + 8 * ac) && ok;
+                ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, parity, rank, dead,
+                                         acc_empty + 8 * ac.stage) && ok;
             } else {
                 if (ok) write_tile<T, Chunk<T, BN>::kTokens>(a, tl, acc, S, part);
                 tc_fence_before();
                 tile_bar();
-                if (threadIdx.x == 128) mbar_arrive(acc_empty + 8 * ac);
+                if (threadIdx.x == 128) mbar_arrive(acc_empty + 8 * ac.stage);
             }
         }
     }

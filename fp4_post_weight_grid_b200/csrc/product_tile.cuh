@@ -106,6 +106,14 @@ __device__ __forceinline__ void split_steps(const TileArgs& a, int rank, int& fi
     last = (int)((int64_t)a.k_steps * (rank + 1) / a.split);
 }
 
+// For a dead thread block: the last copies into a ring, whose phases may not
+// have been waited for, end before the block does.
+template <int N> __device__ __forceinline__ void drain_ring(Ring<N> r, uint32_t full, volatile int* dead)
+{
+    if (!*dead) return;
+    for (int i = 0; i < N; ++i, r.next()) mbar_drain(full + 8 * r.stage, r.parity ^ 1);
+}
+
 // From the accumulator (lane = feature, column = token) to y, by four warps
 // that each own a quarter of the lanes, kChunk tokens at a time through
 // shared memory: a thread writes its feature's sums of the chunk there (rows

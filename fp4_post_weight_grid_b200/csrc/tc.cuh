@@ -14,6 +14,32 @@ namespace fp4q {
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
+// One lane of a converged warp.  The warps that feed the tensor cores run their
+// loops converged and issue under this predicate: addresses and descriptors
+// then stay in the warp's uniform registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
+
+// A place in a ring of N stages and the parity of its current pass.
+template <int N> struct Ring {
+    uint32_t stage = 0, parity = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++stage == N) {
+            stage = 0;
+            parity ^= 1;
+        }
+    }
+};
+
 // ---------------------------------------------------------------- mbarriers
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
 {
