@@ -50,40 +50,79 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
     return r;
 }
 
-// Eight codes -> four pairs of bf16 in column order, each q * 2^-126: the three
-// magnitude bits of a code put where bf16 keeps the low exponent bits and the
-// first mantissa bit are its value under an exponent bias of 127 instead of 1
-// (the code 1/2 becomes a subnormal, which the multiplication takes exactly).
-__device__ __forceinline__ void decode8(uint32_t w, uint32_t scale, uint32_t* out)
+template <uint32_t kSel> __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b)
 {
-    const uint32_t up = w << 4;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        // high byte of the low half: the low nibble of byte j, of the high half: the high nibble
-        const uint32_t p = __byte_perm(up, w, j | j << 4 | (4 + j) << 8 | (4 + j) << 12);
-        out[j] = mul_bf16x2((p & 0x80008000u) | ((p >> 6) & 0x01C001C0u), scale);
-    }
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "n"(kSel));
+    return r;
 }
 
-// The factor for decode8 of an E4M3 byte, in both halves: s * 2^119 (the
-// decoded weight is q * s * 2^-7, in range for every q and s).
-__device__ __forceinline__ uint32_t nv_factor(uint32_t byte)
+// Eight codes -> four pairs of bf16 in column order, each q * 2^-126 times its
+// half of `scale`.  Where bf16 keeps the low exponent bits and the first
+// mantissa bit (8..6), the three magnitude bits of a code are its value under
+// an exponent bias of 127 instead of 1 (the code 1/2 becomes a subnormal,
+// which the multiplication takes exactly); the sign goes to bit 15.  A pair's
+// nibbles come to bits 3..0 of the two halves (the permutation's sign mode
+// gives the zero bytes between them), one integer multiplication by 2^6 + 2^12
+// puts both copies of each in place, and a mask keeps the bits wanted: two
+// operations of the ALU pipe a pair, which is what bounds the decoding, where
+// shifting and merging took four (212 -> 125 ALU instructions per warp and step).
+template <int J> __device__ __forceinline__ uint32_t decode2(uint32_t lo, uint32_t hi, uint32_t scale)
 {
-    const uint32_t h = (byte & 0x7F) << 4, both = h | h << 16;             // s * 2^-120
-    const uint32_t f = mul_bf16x2(mul_bf16x2(both, 0x7F007F00u), 0x77807780u);   // * 2^127 * 2^112
-    return (byte & 0x7F) == 0x7F ? 0x7FC07FC0u : f;
+    const uint32_t p = prmt<J | (J | 8) << 4 | (4 + J) << 8 | (12 + J) << 12>(lo, hi);
+    return mul_bf16x2((p * 0x1040u) & 0x81C081C0u, scale);
 }
-// Of an E8M0 byte: 2^(b-127-2+126) up to b = 130, where the product is
-// q * 2^(b-129); what is above 130 is left to mx_rest.
-__device__ __forceinline__ uint32_t mx_factor(uint32_t byte)
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t scale, uint32_t* out)
 {
-    const uint32_t h = (min(byte, 130u) + 124) << 7;
-    return h | h << 16;
+    const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+    out[0] = decode2<0>(lo, hi, scale);
+    out[1] = decode2<1>(lo, hi, scale);
+    out[2] = decode2<2>(lo, hi, scale);
+    out[3] = decode2<3>(lo, hi, scale);
 }
-__device__ __forceinline__ uint32_t mx_rest(uint32_t byte)
+
+// 64 columns of one row: 32 bytes of codes, and their scales.
+//
+// NVFP4, four E4M3 bytes: the factors are s * 2^119 (from bits 10..4 of a
+// half, where a byte stands for s * 2^-120, in two exact multiplications); the
+// decoded weight is q * s * 2^-7, in range for every q and s.
+__device__ __forceinline__ void decode_nvfp4(const uint32_t (&c)[8], uint32_t scales, uint32_t (&r)[32])
 {
-    const uint32_t h = byte == 255 ? 0x7FC0u : (byte - 130 + 127) << 7;
-    return h | h << 16;
+    const uint32_t s = scales & 0x7F7F7F7Fu;
+    uint32_t f[2] = {prmt<0x4140>(s, 0) << 4, prmt<0x4342>(s, 0) << 4};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) f[i] = mul_bf16x2(mul_bf16x2(f[i], 0x7F007F00u), 0x77807780u);      // * 2^127 * 2^112
+    if ((s + 0x01010101u) & 0x80808080u) {                 // a byte 0x7F is a NaN
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (((s >> (8 * i)) & 0x7F) == 0x7F) f[i / 2] |= 0x7FFFu << (16 * (i % 2));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t both = i % 2 ? prmt<0x3232>(f[i / 2], 0) : prmt<0x1010>(f[i / 2], 0);
+        decode8(c[2 * i], both, r + 8 * i);
+        decode8(c[2 * i + 1], both, r + 8 * i + 4);
+    }
+}
+// MXFP4, the two E8M0 bytes in the low half of `scales`: the factors are
+// 2^(b-129+126) up to b = 130, and the decoded weight q * 2^(b-129), which is in
+// range up to b = 254; above 130 what is missing multiplies the result.
+__device__ __forceinline__ void decode_mxfp4(const uint32_t (&c)[8], uint32_t scales, uint32_t (&r)[32])
+{
+    const uint32_t b = prmt<0x4140>(scales, 0);
+    const bool large = ((b + 0x007D007Du) & 0x01000100u) != 0;         // a byte above 130
+    const uint32_t f = (large ? __vminu2(b, 0x00820082u) : b) * 128u + 0x3E003E00u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) decode8(c[i], i < 4 ? prmt<0x1010>(f, 0) : prmt<0x3232>(f, 0), r + 4 * i);
+    if (large) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t e = (b >> (16 * i)) & 255;
+            const uint32_t h = e == 255 ? 0x7FC0u : (max(e, 130u) - 130 + 127) << 7;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) r[16 * i + q] = mul_bf16x2(r[16 * i + q], h | h << 16);
+        }
+    }
 }
 
 // D[128][N] (+)= A[128][16] * B[N][16]^T, bf16, A in tensor memory.
@@ -283,26 +322,10 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                     const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + (MX ? i / 2 : i) * 512);
                     const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
                     uint32_t r[32];
-                    if (MX) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t b = (sc >> (16 * (i & 1) + 8 * h)) & 255, f = mx_factor(b);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) decode8(c[4 * h + q], f, r + 16 * h + 4 * q);
-                            if (b > 130) {
-                                const uint32_t f2 = mx_rest(b);
-#pragma unroll
-                                for (int q = 0; q < 16; ++q) r[16 * h + q] = mul_bf16x2(r[16 * h + q], f2);
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            const uint32_t f = nv_factor((sc >> (8 * h)) & 255);
-                            decode8(c[2 * h], f, r + 8 * h);
-                            decode8(c[2 * h + 1], f, r + 8 * h + 4);
-                        }
-                    }
+                    if (MX)
+                        decode_mxfp4(c, sc >> (16 * (i & 1)), r);
+                    else
+                        decode_nvfp4(c, sc, r);
                     const uint32_t as = group * C::kADepth + d.stage;
                     if (!(ok = mbar_wait(a_empty + 8 * as, d.parity ^ 1, dead))) break;
                     tc_fence_after();
@@ -361,7 +384,7 @@ template <bool MX, int BN, typename T> static cudaError_t launch_one(const Produ
 template <bool MX, typename T> static cudaError_t launch_shape(const Product& p, cudaStream_t s)
 {
     TileArgs a = tile_args(p, kStepCols, MX ? 128 : 64);
-    const TileShape shape = tile_shape(p, a.n_tiles, a.k_steps);
+    const TileShape shape = tile_shape(p, a.n_tiles, a.k_steps, Config<16>::kResident);
     switch (shape.tokens) {
     case 16: return launch_one<MX, 16, T>(p, a, shape.split, s);
     case 32: return launch_one<MX, 32, T>(p, a, shape.split, s);

@@ -267,7 +267,7 @@ template <bool MX, int BN, typename T> static cudaError_t launch_one(const Produ
 template <bool MX, typename T> static cudaError_t launch_shape(const Product& p, cudaStream_t s)
 {
     TileArgs a = tile_args(p, kStepCols, MX ? 128 : 64);
-    const TileShape shape = tile_shape(p, a.n_tiles, a.k_steps);
+    const TileShape shape = tile_shape(p, a.n_tiles, a.k_steps, Config<16>::kResident);
     switch (shape.tokens) {
     case 16: return launch_one<MX, 16, T>(p, a, shape.split, s);
     case 32: return launch_one<MX, 32, T>(p, a, shape.split, s);

@@ -63,7 +63,7 @@ TileArgs tile_args(const Product& p, int step_cols, int scale_tile_cols)
     return a;
 }
 
-TileShape tile_shape(const Product& p, int n_tiles, int k_steps)
+TileShape tile_shape(const Product& p, int n_tiles, int k_steps, int few_per_sm)
 {
     const int64_t rows = p.offsets ? (p.m + p.groups - 1) / p.groups : p.m;       // of a group, on average
     const int64_t busy = p.offsets ? std::min<int64_t>(p.groups, p.m) : 1;
@@ -73,7 +73,7 @@ TileShape tile_shape(const Product& p, int n_tiles, int k_steps)
     auto tiles = [&] { return busy * ((rows + t.tokens - 1) / t.tokens) * n_tiles; };
     while (t.tokens > 32 && tiles() < sms) t.tokens /= 2;
     if (t.tokens <= 64) {
-        const int64_t slots = (int64_t)sms * (t.tokens <= 32 ? 2 : 1);
+        const int64_t slots = (int64_t)sms * (t.tokens <= 32 ? few_per_sm : 1);
         while (t.split < 8 && t.split * 2 <= k_steps && tiles() * t.split * 2 <= slots) t.split *= 2;
     }
     return t;

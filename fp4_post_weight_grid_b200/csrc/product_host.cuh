@@ -20,7 +20,8 @@ struct TileShape {
     int tokens;      // BN: 16, 32, 64, 128 or 256
     int split;       // thread blocks that share a tile's K
 };
-TileShape tile_shape(const Product& p, int n_tiles, int k_steps);
+// few_per_sm: resident thread blocks per SM of the shapes of 16 and 32 tokens.
+TileShape tile_shape(const Product& p, int n_tiles, int k_steps, int few_per_sm);
 
 // One launch over all tiles: as many clusters of `split` thread blocks as are
 // resident at once (or as there are tiles, if fewer), each striding over the
