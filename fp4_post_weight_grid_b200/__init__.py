@@ -564,42 +564,63 @@ def fp4q_dequant(fmt: int, codes, scales, d_global_scale, rows: int, cols: int, 
            "fp4q_dequant")
 
 
+def _ptr(t, name, dtype, numel, device):
+    """_dev for the products, whose calls are short enough for the checks to
+    count: the same checks, in one comparison while nothing is wrong."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.device == device and t.is_contiguous()
+            and (numel is None or t.numel() == numel) and device.type == "cuda"):
+        return t.data_ptr() or None
+    return _dev(t, name, dtype, numel, device)
+
+
 def _product(name, fmt, x, x_scales, x_global_scale, offsets, w_codes, w_scales, w_global_scale, y, d_status, bias,
              act, mul, residual, stream):
     """Checks and marshalling of the four products.  x_scales None: x is bf16;
     offsets None: one weight."""
-    if fmt not in (NVFP4, MXFP4):
+    if fmt != NVFP4 and fmt != MXFP4:
         raise Fp4qError(ERR_DTYPE, name)
-    block = MXFP4_BLOCK if fmt == MXFP4 else NVFP4_BLOCK
-    dev, packed, grouped = y.device, x_scales is not None, offsets is not None
-    if x.dim() != 2 or y.dim() != 2 or w_codes.dim() != (3 if grouped else 2):
+    nv, packed, grouped = fmt == NVFP4, x_scales is not None, offsets is not None
+    block = NVFP4_BLOCK if nv else MXFP4_BLOCK
+    dev, dt, ws, xs, ys = y.device, y.dtype, w_codes.shape, x.shape, y.shape
+    if len(xs) != 2 or len(ys) != 2 or len(ws) != (3 if grouped else 2):
         raise ValueError(f"{name}: x and y are 2-D, w_codes {'[groups, n, k/2]' if grouped else '[n, k/2]'}")
-    groups = w_codes.shape[0] if grouped else 1
-    n, k, m = w_codes.shape[-2], 2 * w_codes.shape[-1], x.shape[0]
-    if x.shape[1] != (k // 2 if packed else k) or y.shape[0] != m or y.shape[1] != n:
-        raise ValueError(f"{name}: x {tuple(x.shape)}, w_codes {tuple(w_codes.shape)} and y {tuple(y.shape)} do not fit")
+    groups, n, k, m = ws[0] if grouped else 1, ws[-2], 2 * ws[-1], xs[0]
+    if xs[1] != (k // 2 if packed else k) or ys[0] != m or ys[1] != n:
+        raise ValueError(f"{name}: x {tuple(xs)}, w_codes {tuple(ws)} and y {tuple(ys)} do not fit")
     if k == 0 or k % 32:
         raise Fp4qError(ERR_SHAPE, f"{name}: k = {k} is not a positive multiple of 32")
-    lib = load()
-    nv, dt = fmt == NVFP4, y.dtype
     if nv and (w_global_scale is None or (packed and x_global_scale is None)):
         raise Fp4qError(ERR_NULL, f"{name}: NVFP4 needs its global scales")
-    ep = Epilogue(_dev(bias, "bias", dt, groups * n, dev), _dev(mul, "mul", dt, m * n, dev),
-                  _dev(residual, "residual", dt, m * n, dev), int(act))
-    args = [int(fmt), _dev(x, "x", torch.uint8 if packed else torch.bfloat16, None, dev)]
+    ep = None
+    if bias is not None or mul is not None or residual is not None or act:
+        ep = ctypes.byref(Epilogue(None if bias is None else _ptr(bias, "bias", dt, groups * n, dev),
+                                   None if mul is None else _ptr(mul, "mul", dt, m * n, dev),
+                                   None if residual is None else _ptr(residual, "residual", dt, m * n, dev), act))
+    yp, code = _ptr(y, "y", dt, None, dev), _wdtype(y)
+    xp = _ptr(x, "x", torch.uint8 if packed else torch.bfloat16, None, dev)
+    wp = _ptr(w_codes, "w_codes", torch.uint8, None, dev)
+    # fp4q_mma_scale_bytes(n, k / block) per group
+    wsp = _ptr(w_scales, "w_scales", torch.uint8, groups * (-(-n // 128)) * (-(-k // (4 * block))) * 512, dev)
+    gp = _ptr(w_global_scale, "w_global_scale", torch.float32, groups, dev) if nv else None
+    sp = _ptr(d_status, "d_status", torch.int32, 1, dev)
     if packed:
-        args += [_dev(x_scales, "x_scales", torch.uint8, m * (k // block), dev),
-                 _dev(x_global_scale, "x_global_scale", torch.float32, 1, dev) if nv else None]
-    args.append(m)
+        head = (fmt, xp, _ptr(x_scales, "x_scales", torch.uint8, m * (k // block), dev),
+                _ptr(x_global_scale, "x_global_scale", torch.float32, 1, dev) if nv else None, m)
+    else:
+        head = (fmt, xp, m)
     if grouped:
-        args += [_dev(offsets, "offsets", torch.int32, groups + 1, dev), groups]
-    args += [_dev(w_codes, "w_codes", torch.uint8, None, dev),
-             _dev(w_scales, "w_scales", torch.uint8, groups * int(lib.fp4q_mma_scale_bytes(n, k // block)), dev),
-             _dev(w_global_scale, "w_global_scale", torch.float32, groups, dev) if nv else None,
-             n, k, ctypes.byref(ep), _dev(y, "y", None, None, dev), _wdtype(y),
-             _dev(d_status, "d_status", torch.int32, 1, dev)]
-    with torch.cuda.device(dev):
-        _check(getattr(lib, name)(*args, _stream(stream)), name)
+        head += (_ptr(offsets, "offsets", torch.int32, groups + 1, dev), groups)
+    fn = getattr(load(), name)
+    here = torch.cuda.current_device()
+    if dev.index == here:
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(here)
+        status = fn(*head, wp, wsp, gp, n, k, ep, yp, code, sp, stream if type(stream) is int else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*head, wp, wsp, gp, n, k, ep, yp, code, sp, _stream(stream))
+    if status:
+        raise Fp4qError(status, name)
 
 
 def fp4q_linear(fmt: int, x, w_codes, w_scales, w_global_scale, y, d_status, bias=None, act: int = ACT_NONE, mul=None,
