@@ -13,7 +13,7 @@
 //   warp 1     one thread issues the products, 4 of 16 columns per step of x;
 //   warp 2     the tile table, then idle;
 //   warps 4..  DQ groups of four decode, a step of 64 columns at a time;
-//   the last 4 take the accumulator to y (product_tile.cuh).
+//   the last   in groups of four, take the accumulator to y (product_tile.cuh).
 #include "product_host.cuh"
 
 namespace fp4q {
@@ -26,18 +26,19 @@ constexpr int kACols = kSubCols / 2;       // columns of tensor memory per decod
 
 template <int BN> struct Config {
     static constexpr int kW = 128 * 128, kWStage = kW + 4 * 512, kX = BN * 128;
-    static constexpr int kWStages = BN >= 256 ? 2 : BN >= 128 ? 5 : BN >= 64 ? 7 : 8;
-    static constexpr int kXStages = BN >= 256 ? 5 : BN >= 128 ? 6 : BN >= 64 ? 4 : 8;
-    static constexpr int kAccs = BN <= 128 ? 2 : 1;
+    static constexpr int kWStages = BN > 128 ? 3 : BN > 64 ? 5 : BN > 32 ? 7 : 8;
+    static constexpr int kXStages = BN > 64 ? 4 : BN > 32 ? 4 : 8;
+    static constexpr int kAccs = 2;
     static constexpr int kDq = BN <= 64 ? 4 : 2;                    // groups of four decoding warps
-    static constexpr int kThreads = (4 + 4 * kDq + 4) * 32;
+    static constexpr int kEpi = BN > 64 ? 2 : 1;                    // groups of four epilogue warps
+    static constexpr int kThreads = (4 + 4 * kDq + 4 * kEpi) * 32;
     static constexpr int kADepth = 2;                               // decoded steps in tensor memory, per group
     static constexpr int kASteps = kDq * kADepth;
     static constexpr int kUsed = kAccs * BN + kASteps * kACols;
     static constexpr int kCols = kUsed <= 256 ? 256 : 512;
     static constexpr bool kSplits = BN <= 64;
-    static constexpr int kPart = (kSplits ? BN : 32) * kPartRow * 4;        // sums on their way to y
-    static constexpr int kSmem = kWStages * kWStage + kXStages * kX + kPart + 1024;
+    static constexpr int kPart = (kSplits ? BN : 32) * kPartRow * 4;        // sums on their way to y, per group
+    static constexpr int kSmem = kWStages * kWStage + kXStages * kX + kEpi * kPart + 1024;
     static constexpr int kResident = 1;
     static_assert(kUsed <= 512 && kCols * kResident <= 512, "tensor memory");
     static_assert(kSmem <= 222 * 1024 && kWStage % 1024 == 0 && kX % 1024 == 0, "shared memory");
@@ -192,7 +193,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             }
             for (int i = 0; i < C::kAccs; ++i) {
                 mbar_init(acc_full + 8 * i, 1);
-                mbar_init(acc_empty + 8 * i, 1);
+                mbar_init(acc_empty + 8 * i, C::kEpi);
             }
             mbar_init(part_full, a.split);
             mbar_init(part_empty, a.split);
@@ -202,9 +203,9 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             tma_prefetch_desc(&x_map);
         }
     } else if (warp == 1) {
-        tmem_alloc(smem_u32(&tmem_slot), C::kCols);
+        tmem_alloc<1>(smem_u32(&tmem_slot), C::kCols);
     } else if (warp == 2) {
-        const bool ok = tile_table<BN>(a, before);
+        const bool ok = tile_table(a, before);
         if (lane == 0) good_offsets = ok;
     }
     tc_fence_before();
@@ -225,7 +226,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         Ring<C::kWStages> w;
         bool ok = true;
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-            const Tile tl = tile_at<BN>(a, before, t);
+            const Tile tl = tile_at<128>(a, before, t);
             const int wrow = (int)(tl.group * a.n) + tl.feature;
             const uint8_t* ws = a.w_scales + tl.group * a.w_scale_stride +
                                 (int64_t)(tl.feature / 128) * a.w_col_tiles * 512;
@@ -247,13 +248,13 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         Ring<C::kXStages> x;
         bool ok = true;
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-            const Tile tl = tile_at<BN>(a, before, t);
+            const Tile tl = tile_at<128>(a, before, t);
             const int c1 = min(a.k, k1 * kStepCols);
             for (int c = k0 * kStepCols; c < c1; c += kSubCols, x.next()) {
                 if (!(ok = mbar_wait(x_empty + 8 * x.stage, x.parity ^ 1, dead))) break;
                 const uint32_t bar = x_full + 8 * x.stage;
                 if (elect_one()) {
-                    mbar_expect(bar, C::kX);
+                    mbar_expect(bar, a.tokens * 128);
                     tma_load(smem_u32(x_ring) + x.stage * C::kX, &x_map, c * 2, tl.row, bar);
                 }
                 __syncwarp();
@@ -267,7 +268,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         bool ok = true;
         const uint64_t desc0 = desc_k128(smem_u32(x_ring));
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next()) {
-            const Tile tl = tile_at<BN>(a, before, t);
+            const Tile tl = tile_at<128>(a, before, t);
             const uint32_t idesc = idesc_bf16(min(BN, (tl.rows + 15) / 16 * 16));
             const uint32_t acc = tmem + ac.stage * BN;
             if (!(ok = mbar_wait(acc_empty + 8 * ac.stage, ac.parity ^ 1, dead))) break;
@@ -288,19 +289,19 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                         for (int c = 0; c < kSubCols / 16; ++c)
                             tc_mma_bf16(acc, a_tmem + as * kACols + c * 8, desc0 + x.stage * (C::kX >> 4) + c * 2,
                                         idesc, k > k0 || i > 0 || c > 0);
-                        tc_commit(a_empty + 8 * as);
-                        tc_commit(x_empty + 8 * x.stage);
+                        tc_commit<1>(a_empty + 8 * as);
+                        tc_commit<1>(x_empty + 8 * x.stage);
                     }
                     __syncwarp();
                     d.next();
                     x.next();
                 }
             }
-            if (elect_one()) tc_commit(acc_full + 8 * ac.stage);
+            if (elect_one()) tc_commit<1>(acc_full + 8 * ac.stage);
             __syncwarp();
         }
         if (*dead) {
-            if (elect_one()) tc_commit(drain);
+            if (elect_one()) tc_commit<1>(drain);
             mbar_drain(drain, 0);
         }
     } else if (warp >= 4 && warp < 4 + 4 * C::kDq) {
@@ -339,11 +340,12 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             }
         }
     } else if (warp >= 4 + 4 * C::kDq) {
+        const int e = (warp - 4 - 4 * C::kDq) / 4;
         Ring<C::kAccs> ac;
         uint32_t parity = 0;
         bool ok = true;
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next(), parity ^= 1) {
-            const Tile tl = tile_at<BN>(a, before, t);
+            const Tile tl = tile_at<128>(a, before, t);
             const uint32_t acc = tmem + ac.stage * BN;
             const float S = MX ? 4.f : a.w_S[tl.group] * 128.f;        // the decoded weights are scaled down
             ok = mbar_wait(acc_full + 8 * ac.stage, ac.parity, dead);
@@ -352,9 +354,9 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, parity, rank, dead,
                                          acc_empty + 8 * ac.stage) && ok;
             } else {
-                if (ok) write_tile<T, Chunk<T, BN>::kTokens>(a, tl, acc, S, part);
+                if (ok) write_tile<T, Chunk<T, BN>::kTokens, C::kEpi>(a, tl, acc, S, part + e * (C::kPart / 4), e);
                 tc_fence_before();
-                tile_bar();
+                tile_bar(e);
                 if (warp % 4 == 0 && lane == 0) mbar_arrive(acc_empty + 8 * ac.stage);
             }
         }
@@ -362,36 +364,35 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_free(tmem, C::kCols);
+    if (warp == 1) tmem_free<1>(tmem, C::kCols);
     if (threadIdx.x == 0 && *dead) atomicOr(a.status, FP4Q_FLAG_TIMEOUT);
     if (a.split > 1) cluster_sync_all();       // a peer may still read this block's partial sums
 }
 
 }  // namespace
 
-template <bool MX, int BN, typename T> static cudaError_t launch_one(const Product& p, TileArgs& a, int split, cudaStream_t s)
+template <bool MX, int BN, typename T>
+static cudaError_t launch_one(const Product& p, TileArgs& a, const TileShape& shape, cudaStream_t s)
 {
     using C = Config<BN>;
     auto kernel = linear_kernel<MX, BN, T>;
     CUtensorMap w_map, x_map;
     cudaError_t e = byte_tile_map(&w_map, p.w, p.n * p.groups, p.k / 2, 128);
-    if (e == cudaSuccess) e = byte_tile_map(&x_map, p.x, p.m, p.k * 2, BN);
+    if (e == cudaSuccess) e = byte_tile_map(&x_map, p.x, p.m, p.k * 2, shape.tokens);
     if (e != cudaSuccess) return e;
     const int per_sm = resident_blocks_per_sm(reinterpret_cast<const void*>(kernel), C::kThreads, C::kSmem);
-    return launch_tiles(kernel, w_map, x_map, p, a, BN, split, per_sm, C::kThreads, C::kSmem, s);
+    return launch_tiles(kernel, w_map, x_map, p, a, shape, 1, per_sm, C::kThreads, C::kSmem, s);
 }
 
 template <bool MX, typename T> static cudaError_t launch_shape(const Product& p, cudaStream_t s)
 {
     TileArgs a = tile_args(p, kStepCols, MX ? 128 : 64);
-    const TileShape shape = tile_shape(p, a.n_tiles, a.k_steps, Config<16>::kResident);
-    switch (shape.tokens) {
-    case 16: return launch_one<MX, 16, T>(p, a, shape.split, s);
-    case 32: return launch_one<MX, 32, T>(p, a, shape.split, s);
-    case 64: return launch_one<MX, 64, T>(p, a, shape.split, s);
-    case 128: return launch_one<MX, 128, T>(p, a, 1, s);
-    default: return launch_one<MX, 256, T>(p, a, 1, s);
-    }
+    const TileShape shape = tile_shape(p, a.k_steps, 1, Config<16>::kResident);
+    if (shape.tokens <= 16) return launch_one<MX, 16, T>(p, a, shape, s);
+    if (shape.tokens <= 32) return launch_one<MX, 32, T>(p, a, shape, s);
+    if (shape.tokens <= 64) return launch_one<MX, 64, T>(p, a, shape, s);
+    if (shape.tokens <= 128) return launch_one<MX, 128, T>(p, a, shape, s);
+    return launch_one<MX, 192, T>(p, a, shape, s);
 }
 
 cudaError_t launch_linear(const Product& p, cudaStream_t s)

@@ -4,53 +4,62 @@
 // One thread block works on tiles of 128 features x BN tokens (product_tile.cuh)
 // in steps of 256 columns, in four roles that meet at mbarriers:
 //   warp 0     copies the codes of both operands (128-byte rows, swizzled) and
-//              the weight's tiled scales into a ring of STAGES steps;
+//              the weight's tiled scales into a ring of kStages steps;
 //   warps 2-3  copy the tokens' row-major scales into the tiled layout of the
 //              ring, 4 bytes (one row of a tile) at a time;
-//   warp 1     one thread moves a step's scales to tensor memory and issues
-//              four products of 64 columns;
-//   warps 4-7  take the accumulator to y.
+//   warp 1     moves a step's scales to tensor memory and issues four products
+//              of 64 columns;
+//   warps 4..  in groups of four, take the accumulator to y.
 // The products are exact (2 x 2 significant bits, block scales of 4 x 4) and
 // summed in binary32 in tensor memory; the global scales multiply the sum.
-#include "launch.h"
-#include "product.h"
+//
+// Many tokens: two thread blocks of a cluster share a tile of 256 features x
+// 192 tokens.  Each holds its 128 features and half of the tokens' codes, and
+// the tensor cores of both read both halves, so that a step brings 16 + 12 KB
+// to an SM where a tile of its own (128 x 192) would bring 16 + 24 KB for the
+// same products: what bounds the wide tiles is the way from L2.  Two
+// accumulators of 192 columns let the epilogue of one tile run under the
+// products of the next.
 #include "product_host.cuh"
 
 namespace fp4q {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kStepCols = 256;             // columns of a step: 128 bytes of codes
 constexpr int kMmaCols = 64;
 
 template <int BN> struct Config {
+    static constexpr int kPair = BN > 128 ? 2 : 1;                  // thread blocks of a tile
     static constexpr int kTokenTiles = (BN + 127) / 128;            // scale tiles over the tokens
-    static constexpr int kW = 128 * 128, kX = BN * 128;             // bytes of a step
+    static constexpr int kW = 128 * 128, kX = BN / kPair * 128;     // bytes of a step
     static constexpr int kWS = 4 * 512, kXS = kTokenTiles * 4 * 512;
     static constexpr int kStage = kW + kX + kWS + kXS;
-    static constexpr int kStages = BN == 128 ? 5 : BN == 32 || BN == 256 ? 3 : 4;
-    static constexpr int kAccs = BN <= 128 ? 2 : 1;
-    // tensor memory: accumulators, then per stage the scales of 4 products
+    static constexpr int kStages = BN > 32 ? 5 : BN == 32 ? 3 : 4;
+    static constexpr int kAccs = 2;
+    // Tensor memory: accumulators, then the scales of the last two steps.
     static constexpr int kScaleCols = 4 * 4 * (1 + kTokenTiles);
-    static constexpr int kUsed = kAccs * BN + kStages * kScaleCols;
+    static constexpr int kUsed = kAccs * BN + 2 * kScaleCols;
     static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     static constexpr bool kSplits = BN <= 64;
-    static constexpr int kPart = (kSplits ? BN : 32) * kPartRow * 4;        // sums on their way to y
-    static constexpr int kSmem = kStages * kStage + kPart + 1024;
+    static constexpr int kEpi = BN >= 128 ? 2 : 1;                  // groups of four epilogue warps
+    static constexpr int kPart = (kSplits ? BN : 32) * kPartRow * 4;        // sums on their way to y, per group
+    static constexpr int kThreads = (4 + 4 * kEpi) * 32;
+    static constexpr int kSmem = kStages * kStage + kEpi * kPart + 1024;
     static constexpr int kResident = BN <= 32 ? 2 : 1;
     static_assert(kUsed <= 512 && kCols * kResident <= 512, "tensor memory");
-    static_assert(kSmem <= 227 * 1024 && kStage % 1024 == 0, "shared memory");
+    static_assert(kSmem <= 222 * 1024 && kStage % 1024 == 0, "shared memory");
 };
 
 template <bool MX, int BN, typename T>
-__global__ void __launch_bounds__(kThreads, Config<BN>::kResident)
+__global__ void __launch_bounds__(Config<BN>::kThreads, Config<BN>::kResident)
 matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
               const __grid_constant__ TileArgs a)
 {
     using C = Config<BN>;
+    constexpr int G = C::kPair;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t bars[2 * C::kStages + 2 * C::kAccs + 3];
+    __shared__ __align__(8) uint64_t bars[3 * C::kStages + 2 * C::kAccs + 3];
     __shared__ int before[FP4Q_PRODUCT_GROUPS_MAX + 1];
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_word, good_offsets;
@@ -60,21 +69,23 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     uint8_t* ring = raw + (1024 - smem_u32(raw) % 1024) % 1024;
     float* part = reinterpret_cast<float*>(ring + C::kStages * C::kStage);
     const uint32_t ring0 = smem_u32(ring);
-    const uint32_t full = smem_u32(bars), empty = full + 8 * C::kStages, acc_full = empty + 8 * C::kStages,
-                   acc_empty = acc_full + 8 * C::kAccs, part_full = acc_empty + 8 * C::kAccs, part_empty = part_full + 8,
-                   drain = part_empty + 8;
-    const uint32_t rank = a.split > 1 ? cluster_rank() : 0;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * C::kStages, peer_full = empty + 8 * C::kStages,
+                   acc_full = peer_full + 8 * C::kStages, acc_empty = acc_full + 8 * C::kAccs,
+                   part_full = acc_empty + 8 * C::kAccs, part_empty = part_full + 8, drain = part_empty + 8;
+    const bool cluster = G > 1 || a.split > 1;
+    const uint32_t rank = cluster ? cluster_rank() : 0;
 
     if (warp == 0) {
         if (lane == 0) {
             dead_word = 0;
             for (int i = 0; i < C::kStages; ++i) {
-                mbar_init(full + 8 * i, 1 + 2);            // the copies, two warps of token scales
+                mbar_init(full + 8 * i, 1 + 64);           // the copies, the threads of the token scales
                 mbar_init(empty + 8 * i, 1);
+                mbar_init(peer_full + 8 * i, 1);
             }
             for (int i = 0; i < C::kAccs; ++i) {
                 mbar_init(acc_full + 8 * i, 1);
-                mbar_init(acc_empty + 8 * i, 1);
+                mbar_init(acc_empty + 8 * i, G * C::kEpi);
             }
             mbar_init(part_full, a.split);
             mbar_init(part_empty, a.split);
@@ -84,149 +95,189 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             tma_prefetch_desc(&x_map);
         }
     } else if (warp == 1) {
-        tmem_alloc(smem_u32(&tmem_slot), C::kCols);
+        tmem_alloc<G>(smem_u32(&tmem_slot), C::kCols);
     } else if (warp == 2) {
-        const bool ok = tile_table<BN>(a, before);
+        const bool ok = tile_table(a, before);
         if (lane == 0) good_offsets = ok;
     }
     tc_fence_before();
     __syncthreads();
-    if (a.split > 1) cluster_sync_all();
+    if (cluster) cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const int64_t tiles = good_offsets ? (int64_t)before[a.groups] * a.n_tiles : 0;
     if (!good_offsets && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, FP4Q_FLAG_OFFSETS);
-    const int64_t first_tile = blockIdx.x / a.split, tile_step = gridDim.x / a.split;
-    constexpr int per_tile = MX ? 128 : 64;                    // columns of a scale tile
+    const int blocks = G > 1 ? G : a.split;                // of a tile
+    const int64_t first_tile = blockIdx.x / blocks, tile_step = gridDim.x / blocks;
+    constexpr int kScaleTile = MX ? 128 : 64;              // columns of a scale tile
+    constexpr int kScaleTiles = kStepCols / kScaleTile;    // of a step
     int k0, k1;
-    split_steps(a, (int)rank, k0, k1);
+    split_steps(a, G > 1 ? 0 : (int)rank, k0, k1);
+    // The tile with this thread block's features.
+    auto my_tile = [&](int64_t t) {
+        Tile r = tile_at<128 * G>(a, before, t);
+        if (G > 1) r.feature += 128 * rank;
+        return r;
+    };
+    // Tokens of a tile as the tensor core counts them.
+    auto mma_cols = [&](const Tile& t) { return (t.rows + 16 * G - 1) / (16 * G) * (16 * G); };
 
     if (warp == 0) {
         Ring<C::kStages> g;
         bool ok = true;
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-            const Tile tl = tile_at<BN>(a, before, t);
+            const Tile tl = my_tile(t);
             const int wrow = (int)(tl.group * a.n) + tl.feature;
-            const uint8_t* ws = a.w_scales + tl.group * a.w_scale_stride +
-                                (int64_t)(tl.feature / 128) * a.w_col_tiles * 512;
+            const int xrow = tl.row + (G > 1 ? (int)rank * (mma_cols(tl) / G) : 0);
+            // Past the last feature (the second half of a pair's tile) any scales will do.
+            const int64_t row_tile = min((int64_t)tl.feature, a.n - 1) / 128;
+            const uint8_t* ws = a.w_scales + tl.group * a.w_scale_stride + row_tile * a.w_col_tiles * 512;
             for (int k = k0; k < k1; ++k, g.next()) {
                 if (!(ok = mbar_wait(empty + 8 * g.stage, g.parity ^ 1, dead))) break;
                 const uint32_t at = ring0 + g.stage * C::kStage, bar = full + 8 * g.stage;
-                const int c0 = k * (kStepCols / per_tile);
-                const uint32_t sb = (uint32_t)min(kStepCols / per_tile, a.w_col_tiles - c0) * 512;
+                const int c0 = k * kScaleTiles;
+                const uint32_t sb = (uint32_t)min(kScaleTiles, a.w_col_tiles - c0) * 512;
                 if (elect_one()) {
-                    mbar_expect(bar, C::kW + C::kX + sb);
+                    mbar_expect(bar, C::kW + a.tokens / G * 128 + sb);
                     tma_load(at, &w_map, k * (kStepCols / 2), wrow, bar);
-                    tma_load(at + C::kW, &x_map, k * (kStepCols / 2), tl.row, bar);
+                    tma_load(at + C::kW, &x_map, k * (kStepCols / 2), xrow, bar);
                     bulk_load(at + C::kW + C::kX, ws + (int64_t)c0 * 512, sb, bar);
                 }
                 __syncwarp();
             }
         }
         drain_ring(g, full, dead);
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank % G != 0) {
+        // The odd block of a pair tells the even one, which issues for both,
+        // that its half of a step is there.
         Ring<C::kStages> g;
-        Ring<C::kAccs> ac;
         bool ok = true;
-        for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next()) {
-            const Tile tl = tile_at<BN>(a, before, t);
-            const uint32_t cols = min(BN, (tl.rows + 15) / 16 * 16);
-            const uint32_t acc = tmem + ac.stage * BN;
-            if (!(ok = mbar_wait(acc_empty + 8 * ac.stage, ac.parity ^ 1, dead))) break;
-            tc_fence_after();
+        for (int64_t t = first_tile; ok && t < tiles; t += tile_step)
             for (int k = k0; k < k1; ++k, g.next()) {
                 if (!(ok = mbar_wait(full + 8 * g.stage, g.parity, dead))) break;
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_peer(peer_full + 8 * g.stage, rank - 1);
+            }
+    } else if (warp == 1) {
+        Ring<C::kStages> g, last2;                         // last2 follows two steps behind
+        Ring<C::kAccs> ac;
+        uint32_t step = 0;
+        bool ok = true;
+        for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next()) {
+            const Tile tl = my_tile(t);
+            const uint32_t cols = mma_cols(tl);
+            const uint32_t acc = tmem + ac.stage * BN;
+            if (!(ok = mbar_wait(acc_empty + 8 * ac.stage, ac.parity ^ 1, dead))) break;
+            for (int k = k0; k < k1; ++k, g.next(), ++step) {
+                ok = mbar_wait(full + 8 * g.stage, g.parity, dead);
+                if (G > 1) ok = ok && mbar_wait(peer_full + 8 * g.stage, g.parity, dead);
+                if (step >= 2) {                           // whose scales were where this step's go
+                    ok = ok && mbar_wait(empty + 8 * last2.stage, last2.parity, dead);
+                    last2.next();
+                }
+                if (!ok) break;
+                fence_async_shared();                      // the token scales
                 tc_fence_after();
                 const uint32_t at = ring0 + g.stage * C::kStage;
-                const uint32_t sf = tmem + C::kAccs * BN + g.stage * C::kScaleCols;
+                const uint32_t sf = tmem + C::kAccs * BN + step % 2 * C::kScaleCols;
                 const int parts = min(kStepCols / kMmaCols, (a.k - k * kStepCols + kMmaCols - 1) / kMmaCols);
                 const uint64_t wd = desc_k128(at), xd = desc_k128(at + C::kW),
                                sd = desc_scales(at + C::kW + C::kX);
                 if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < kStepCols / per_tile; ++i) {
-                        if (i * (per_tile / kMmaCols) >= parts) break;
-                        tc_copy_scales(sf + i * 4, sd + i * (512 >> 4));
+                    for (int i = 0; i < kScaleTiles; ++i) {
+                        if (i * (kScaleTile / kMmaCols) >= parts) break;
+                        tc_copy_scales<G>(sf + i * 4, sd + i * (512 >> 4));
 #pragma unroll
                         for (int h = 0; h < C::kTokenTiles; ++h)
-                            tc_copy_scales(sf + 16 + i * 4 * C::kTokenTiles + h * 4,
-                                           sd + ((C::kWS + (i * C::kTokenTiles + h) * 512) >> 4));
+                            tc_copy_scales<G>(sf + 16 + i * 4 * C::kTokenTiles + h * 4,
+                                              sd + ((C::kWS + (i * C::kTokenTiles + h) * 512) >> 4));
                     }
 #pragma unroll
                     for (int i = 0; i < kStepCols / kMmaCols; ++i) {
                         if (i >= parts) break;
                         const int st = MX ? i / 2 : i;
-                        tc_mma_fp4<MX>(acc, wd + i * 2, xd + i * 2, idesc_fp4(MX, cols, MX ? (i % 2) * 2 : 0),
-                                       sf + st * 4, sf + 16 + st * 4 * C::kTokenTiles, k > k0 || i > 0);
+                        tc_mma_fp4<MX, G>(acc, wd + i * 2, xd + i * 2,
+                                          idesc_fp4(MX, 128 * G, cols, MX ? (i % 2) * 2 : 0), sf + st * 4,
+                                          sf + 16 + st * 4 * C::kTokenTiles, k > k0 || i > 0);
                     }
-                    tc_commit(empty + 8 * g.stage);
+                    tc_commit<G>(empty + 8 * g.stage);
                 }
                 __syncwarp();
             }
-            if (elect_one()) tc_commit(acc_full + 8 * ac.stage);
+            if (elect_one()) tc_commit<G>(acc_full + 8 * ac.stage);
             __syncwarp();
         }
         if (*dead) {
-            if (elect_one()) tc_commit(drain);
+            if (elect_one()) tc_commit<G>(drain);
             mbar_drain(drain, 0);
         }
     } else if (warp < 4) {
         // Token scales: thread i of the 64 takes rows i, i + 64, ...; a row's
         // scales of one tile are 4 neighbouring bytes, at (r % 32) * 16 +
-        // (r / 32) * 4 of that tile.  A step is announced two steps later, when
-        // its copies have landed.
-        constexpr int kLag = 2;
+        // (r / 32) * 4 of that tile.  Where rows start on 4-byte boundaries
+        // they are copied without passing through registers, and the copies
+        // announce themselves; elsewhere the two words around the 4 bytes are
+        // loaded and shifted.
+        constexpr int kRows = (BN + 63) / 64;
         const int i0 = threadIdx.x - 64;
-        const int64_t scols = a.k / (MX ? 32 : 16);
-        const bool words = scols % 4 == 0;                 // rows start on 4-byte boundaries
-        uint32_t it = 0;
+        const int64_t scols = a.k / (MX ? 32 : 16), total = (int64_t)a.m * scols;
+        const bool words = scols % 4 == 0;
+        Ring<C::kStages> g;
         bool ok = true;
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-            const Tile tl = tile_at<BN>(a, before, t);
-            for (int k = k0; k < k1; ++k, ++it) {
-                const uint32_t s = it % C::kStages;
-                if (!(ok = mbar_wait(empty + 8 * s, (it / C::kStages & 1) ^ 1, dead))) break;
-                uint8_t* xs = ring + s * C::kStage + C::kW + C::kX + C::kWS;
-                const int64_t c0 = (int64_t)k * (kStepCols / per_tile) * 4;
-                for (int r = i0; r < BN; r += 64) {
-                    const int64_t row = tl.row + r;
-                    const bool in = row < a.m && r < tl.rows;
-                    const uint8_t* src = a.x_scales + (in ? row * scols : 0);
+            const Tile tl = my_tile(t);
+            for (int k = k0; k < k1; ++k, g.next()) {
+                uint32_t v[kRows][kScaleTiles];
+                const int64_t c0 = (int64_t)k * kScaleTiles * 4;
+                if (!words) {
 #pragma unroll
-                    for (int i = 0; i < kStepCols / per_tile; ++i) {
+                    for (int q = 0; q < kRows; ++q)
+#pragma unroll
+                        for (int i = 0; i < kScaleTiles; ++i) {
+                            const int r = i0 + 64 * q;
+                            const int64_t c = c0 + 4 * i;
+                            v[q][i] = 0;
+                            if (r < tl.rows && c < scols) v[q][i] = load_bytes4(a.x_scales, (tl.row + r) * scols + c, total,
+                                                                                 (int)min((int64_t)4, scols - c));
+                        }
+                }
+                if (!(ok = mbar_wait(empty + 8 * g.stage, g.parity ^ 1, dead))) break;
+                uint8_t* xs = ring + g.stage * C::kStage + C::kW + C::kX + C::kWS;
+#pragma unroll
+                for (int q = 0; q < kRows; ++q) {
+                    const int r = i0 + 64 * q;
+                    if (r >= BN) break;
+                    const bool in = r < tl.rows;
+                    const uint8_t* src = a.x_scales + (in ? (tl.row + r) * scols : 0);
+#pragma unroll
+                    for (int i = 0; i < kScaleTiles; ++i) {
                         uint8_t* dst = xs + (i * C::kTokenTiles + r / 128) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4;
                         const int64_t c = c0 + 4 * i;
                         if (words) {
                             const bool there = in && c < scols;
                             cp_async4(smem_u32(dst), there ? src + c : a.x_scales, there ? 4 : 0);
                         } else {
-                            uint32_t v = 0;
-                            for (int b = 0; b < 4; ++b)
-                                if (in && c + b < scols) v |= (uint32_t)__ldg(src + c + b) << (8 * b);
-                            *reinterpret_cast<uint32_t*>(dst) = v;
+                            *reinterpret_cast<uint32_t*>(dst) = v[q][i];
                         }
                     }
                 }
-                cp_async_commit();
-                if (it >= kLag) {
-                    cp_async_wait<kLag>();
+                if (words) {
+                    cp_async_arrive(full + 8 * g.stage);
+                } else {
                     fence_async_shared();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full + 8 * ((it - kLag) % C::kStages));
+                    mbar_arrive(full + 8 * g.stage);
                 }
             }
         }
-        cp_async_wait<0>();
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0)
-            for (uint32_t i = it < kLag ? 0 : it - kLag; i < it; ++i) mbar_arrive(full + 8 * (i % C::kStages));
     } else {
+        const int e = (warp - 4) / 4;
         Ring<C::kAccs> ac;
         uint32_t parity = 0;
         bool ok = true;
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next(), parity ^= 1) {
-            const Tile tl = tile_at<BN>(a, before, t);
+            const Tile tl = my_tile(t);
             const uint32_t acc = tmem + ac.stage * BN;
             const float S = MX ? 1.f : a.w_S[tl.group] * *a.x_S;
             ok = mbar_wait(acc_full + 8 * ac.stage, ac.parity, dead);
@@ -235,46 +286,50 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, parity, rank, dead,
                                          acc_empty + 8 * ac.stage) && ok;
             } else {
-                if (ok) write_tile<T, Chunk<T, BN>::kTokens>(a, tl, acc, S, part);
+                if (ok) write_tile<T, Chunk<T, BN>::kTokens, C::kEpi>(a, tl, acc, S, part + e * (C::kPart / 4), e);
                 tc_fence_before();
-                tile_bar();
-                if (threadIdx.x == 128) mbar_arrive(acc_empty + 8 * ac.stage);
+                tile_bar(e);
+                if (warp % 4 == 0 && lane == 0) {
+                    if (G > 1)
+                        mbar_arrive_peer(acc_empty + 8 * ac.stage, rank & ~1u);
+                    else
+                        mbar_arrive(acc_empty + 8 * ac.stage);
+                }
             }
         }
     }
     tc_fence_before();
     __syncthreads();
+    if (cluster) cluster_sync_all();           // a peer may still read this block's shared or tensor memory
     tc_fence_after();
-    if (warp == 1) tmem_free(tmem, C::kCols);
+    if (warp == 1) tmem_free<G>(tmem, C::kCols);
     if (threadIdx.x == 0 && *dead) atomicOr(a.status, FP4Q_FLAG_TIMEOUT);
-    if (a.split > 1) cluster_sync_all();       // a peer may still read this block's partial sums
 }
 
 }  // namespace
 
-template <bool MX, int BN, typename T> static cudaError_t launch_one(const Product& p, TileArgs& a, int split, cudaStream_t s)
+template <bool MX, int BN, typename T>
+static cudaError_t launch_one(const Product& p, TileArgs& a, const TileShape& shape, cudaStream_t s)
 {
     using C = Config<BN>;
     auto kernel = matmul_kernel<MX, BN, T>;
     CUtensorMap w_map, x_map;
     cudaError_t e = byte_tile_map(&w_map, p.w, p.n * p.groups, p.k / 2, 128);
-    if (e == cudaSuccess) e = byte_tile_map(&x_map, p.x, p.m, p.k / 2, BN);
+    if (e == cudaSuccess) e = byte_tile_map(&x_map, p.x, p.m, p.k / 2, shape.tokens / C::kPair);
     if (e != cudaSuccess) return e;
-    const int per_sm = resident_blocks_per_sm(reinterpret_cast<const void*>(kernel), kThreads, C::kSmem);
-    return launch_tiles(kernel, w_map, x_map, p, a, BN, split, per_sm, kThreads, C::kSmem, s);
+    const int per_sm = resident_blocks_per_sm(reinterpret_cast<const void*>(kernel), C::kThreads, C::kSmem);
+    return launch_tiles(kernel, w_map, x_map, p, a, shape, C::kPair, per_sm, C::kThreads, C::kSmem, s);
 }
 
 template <bool MX, typename T> static cudaError_t launch_shape(const Product& p, cudaStream_t s)
 {
     TileArgs a = tile_args(p, kStepCols, MX ? 128 : 64);
-    const TileShape shape = tile_shape(p, a.n_tiles, a.k_steps, Config<16>::kResident);
-    switch (shape.tokens) {
-    case 16: return launch_one<MX, 16, T>(p, a, shape.split, s);
-    case 32: return launch_one<MX, 32, T>(p, a, shape.split, s);
-    case 64: return launch_one<MX, 64, T>(p, a, shape.split, s);
-    case 128: return launch_one<MX, 128, T>(p, a, 1, s);
-    default: return launch_one<MX, 256, T>(p, a, 1, s);
-    }
+    const TileShape shape = tile_shape(p, a.k_steps, 2, Config<16>::kResident);
+    if (shape.tokens <= 16) return launch_one<MX, 16, T>(p, a, shape, s);
+    if (shape.tokens <= 32) return launch_one<MX, 32, T>(p, a, shape, s);
+    if (shape.tokens <= 64) return launch_one<MX, 64, T>(p, a, shape, s);
+    if (shape.tokens <= 128) return launch_one<MX, 128, T>(p, a, shape, s);
+    return launch_one<MX, 192, T>(p, a, shape, s);
 }
 
 cudaError_t launch_matmul(const Product& p, cudaStream_t s)

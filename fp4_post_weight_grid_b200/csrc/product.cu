@@ -63,18 +63,35 @@ TileArgs tile_args(const Product& p, int step_cols, int scale_tile_cols)
     return a;
 }
 
-TileShape tile_shape(const Product& p, int n_tiles, int k_steps, int few_per_sm)
+TileShape tile_shape(const Product& p, int k_steps, int pair, int few_per_sm)
 {
     const int64_t rows = p.offsets ? (p.m + p.groups - 1) / p.groups : p.m;       // of a group, on average
     const int64_t busy = p.offsets ? std::min<int64_t>(p.groups, p.m) : 1;
     const int sms = sm_count();
+    auto tiles = [&](int tokens) {
+        const int features = tokens > 128 ? 128 * pair : 128;
+        return busy * ((rows + tokens - 1) / tokens) * ((p.n + features - 1) / features);
+    };
+    // Rounds of tiles over the SMs times the length of one, whose fixed part
+    // is worth about 16 tokens.
+    auto cost = [&](int tokens) {
+        const int64_t slots = tokens > 128 ? sms / pair : sms;
+        return (tiles(tokens) + slots - 1) / slots * (tokens + 16);
+    };
     TileShape t{16, 1};
-    while (t.tokens < 256 && t.tokens < rows) t.tokens *= 2;
-    auto tiles = [&] { return busy * ((rows + t.tokens - 1) / t.tokens) * n_tiles; };
-    while (t.tokens > 32 && tiles() < sms) t.tokens /= 2;
+    while (t.tokens < 128 && t.tokens < rows) t.tokens *= 2;
+    if (rows > 128) {
+        int64_t best = cost(128);
+        for (int tokens = 192; tokens > 128; tokens -= 32)
+            if (cost(tokens) <= best) {
+                best = cost(tokens);
+                t.tokens = tokens;
+            }
+    }
+    while (t.tokens > 32 && tiles(t.tokens) < (t.tokens > 128 ? sms / pair : sms)) t.tokens = t.tokens > 128 ? 128 : t.tokens / 2;
     if (t.tokens <= 64) {
         const int64_t slots = (int64_t)sms * (t.tokens <= 32 ? few_per_sm : 1);
-        while (t.split < 8 && t.split * 2 <= k_steps && tiles() * t.split * 2 <= slots) t.split *= 2;
+        while (t.split < 8 && t.split * 2 <= k_steps && tiles(t.tokens) * t.split * 2 <= slots) t.split *= 2;
     }
     return t;
 }

@@ -17,32 +17,38 @@ cudaError_t byte_tile_map(CUtensorMap* map, const void* base, int64_t rows, int6
 TileArgs tile_args(const Product& p, int step_cols, int scale_tile_cols);
 
 struct TileShape {
-    int tokens;      // BN: 16, 32, 64, 128 or 256
+    int tokens;      // rows of x per tile, a multiple of 16 (of 32 above 128), at most 192
     int split;       // thread blocks that share a tile's K
 };
-// few_per_sm: resident thread blocks per SM of the shapes of 16 and 32 tokens.
-TileShape tile_shape(const Product& p, int n_tiles, int k_steps, int few_per_sm);
+// pair: thread blocks that share a tile of more than 128 tokens; few_per_sm:
+// resident thread blocks per SM of the tiles of up to 32 tokens.
+TileShape tile_shape(const Product& p, int k_steps, int pair, int few_per_sm);
 
-// One launch over all tiles: as many clusters of `split` thread blocks as are
-// resident at once (or as there are tiles, if fewer), each striding over the
-// tiles.  A grouped call knows only how many tiles there can be at most.
+// One launch over all tiles: as many clusters of thread blocks (`pair` or the
+// shape's split) as are resident at once, or as there are tiles, if fewer, each
+// striding over the tiles.  A grouped call knows only how many tiles there can
+// be at most.
 template <typename Kernel>
 cudaError_t launch_tiles(Kernel kernel, const CUtensorMap& w_map, const CUtensorMap& x_map, const Product& p,
-                         TileArgs& a, int tokens, int split, int per_sm, int threads, size_t smem, cudaStream_t s)
+                         TileArgs& a, const TileShape& shape, int pair, int per_sm, int threads, size_t smem,
+                         cudaStream_t s)
 {
-    a.split = split;
-    int64_t token_tiles = (p.m + tokens - 1) / tokens;
-    if (p.offsets) token_tiles = std::min<int64_t>(p.m, p.m / tokens + p.groups);
-    const int64_t slots = std::max<int64_t>(1, (int64_t)sm_count() * per_sm / split);
+    a.tokens = shape.tokens;
+    a.split = shape.split;
+    a.n_tiles = (int)((p.n + 128 * pair - 1) / (128 * pair));
+    int64_t token_tiles = (p.m + a.tokens - 1) / a.tokens;
+    if (p.offsets) token_tiles = std::min<int64_t>(p.m, p.m / a.tokens + p.groups);
+    const int blocks = pair * shape.split;
+    const int64_t slots = std::max<int64_t>(1, (int64_t)sm_count() * per_sm / blocks);
     const int64_t clusters = std::min<int64_t>(token_tiles * a.n_tiles, slots);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(clusters * split));
+    cfg.gridDim = dim3((unsigned)(clusters * blocks));
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.x = (unsigned)blocks;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;

@@ -2,8 +2,8 @@
 // weights share: the list of output tiles, the sum over a cluster that splits
 // K, and the way from tensor memory to y.
 //
-// A tile is 128 rows of W (features) by up to BN rows of x (tokens) of one
-// group.  W is the operand that fills the 128 lanes of tensor memory and the
+// A tile is 128 rows of W (features; 256 where a pair of thread blocks works on
+// it) by up to `tokens` rows of x of one group.  W is the operand that fills the 128 lanes of tensor memory and the
 // tokens are its columns, so that the cost of a tile follows the number of
 // tokens in steps of 16: the same kernel serves one token and thousands.
 #pragma once
@@ -17,7 +17,8 @@ struct TileArgs {
     const int32_t* offsets;       // [groups + 1] or null
     int64_t n;
     int m, k, groups;
-    int n_tiles;                  // tiles of 128 features
+    int n_tiles;                  // tiles of features
+    int tokens;                   // rows of x per tile, at most the kernel's BN
     int k_steps;                  // steps of 256 columns
     int split;                    // thread blocks of the cluster that share a tile's k_steps
     int w_col_tiles;              // scale tiles of a row tile
@@ -36,14 +37,13 @@ struct Tile {
 
 // The token tiles of the groups before each group, in shared memory; built by
 // one warp.  False if the offsets are out of order or range.
-template <int BN>
 __device__ __forceinline__ bool tile_table(const TileArgs& a, int* before)
 {
     const int lane = threadIdx.x & 31;
     if (!a.offsets) {
         if (lane == 0) {
             before[0] = 0;
-            before[1] = (a.m + BN - 1) / BN;
+            before[1] = (a.m + a.tokens - 1) / a.tokens;
         }
         __syncwarp();
         return true;
@@ -56,7 +56,7 @@ __device__ __forceinline__ bool tile_table(const TileArgs& a, int* before)
         if (g < a.groups) {
             const int lo = __ldg(a.offsets + g), hi = __ldg(a.offsets + g + 1);
             ok = ok && lo >= 0 && lo <= hi && hi <= a.m;
-            count = ok ? (hi - lo + BN - 1) / BN : 0;
+            count = ok ? (hi - lo + a.tokens - 1) / a.tokens : 0;
         }
         int sum = count;
         for (int d = 1; d < 32; d *= 2) {
@@ -73,16 +73,16 @@ __device__ __forceinline__ bool tile_table(const TileArgs& a, int* before)
 }
 
 // Tile t: the features vary fastest, so that neighbouring tiles share x.
-template <int BN>
+template <int kFeatures>
 __device__ __forceinline__ Tile tile_at(const TileArgs& a, const int* before, int64_t t)
 {
     const int mt = (int)(t / a.n_tiles);
     Tile r;
-    r.feature = (int)(t % a.n_tiles) * 128;
+    r.feature = (int)(t % a.n_tiles) * kFeatures;
     if (!a.offsets) {
         r.group = 0;
-        r.row = mt * BN;
-        r.rows = min(BN, a.m - r.row);
+        r.row = mt * a.tokens;
+        r.rows = min(a.tokens, a.m - r.row);
         return r;
     }
     int lo = 0, hi = a.groups;            // before[lo] <= mt < before[hi]
@@ -94,9 +94,25 @@ __device__ __forceinline__ Tile tile_at(const TileArgs& a, const int* before, in
             hi = mid;
     }
     r.group = lo;
-    r.row = __ldg(a.offsets + lo) + (mt - before[lo]) * BN;
-    r.rows = min(BN, __ldg(a.offsets + lo + 1) - r.row);
+    r.row = __ldg(a.offsets + lo) + (mt - before[lo]) * a.tokens;
+    r.rows = min(a.tokens, __ldg(a.offsets + lo + 1) - r.row);
     return r;
+}
+
+// `count` (1 to 4) bytes from byte `at` of p, which is 4-byte aligned and has
+// `total` bytes, in the low bytes of a word, zeros above.
+__device__ __forceinline__ uint32_t load_bytes4(const uint8_t* p, int64_t at, int64_t total, int count)
+{
+    const int64_t lo = at & ~3ll;
+    uint32_t v;
+    if (lo + 8 <= total) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(p + lo);
+        v = __funnelshift_r(__ldg(w), __ldg(w + 1), 8 * (int)(at - lo));
+    } else {
+        v = 0;
+        for (int b = 0; b < count; ++b) v |= (uint32_t)__ldg(p + at + b) << (8 * b);
+    }
+    return count < 4 ? v & ((1u << (8 * count)) - 1) : v;
 }
 
 // This thread block's share of a tile's steps.
@@ -124,7 +140,8 @@ template <typename T, int BN> struct Chunk {
     static constexpr int kTokens = BN < 4 * Lanes<T>::kCount ? BN : 4 * Lanes<T>::kCount;
 };
 
-__device__ __forceinline__ void tile_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The barrier of group `e` of four epilogue warps.
+__device__ __forceinline__ void tile_bar(int e) { asm volatile("bar.sync %0, 128;" ::"r"(1 + e) : "memory"); }
 
 // Columns [c0, c0 + count) of the accumulator; S, bias and act are applied
 // on the way where `last` (the sums are complete).
@@ -161,9 +178,10 @@ template <typename T> __device__ __forceinline__ float bias_of(const TileArgs& a
     return a.ep.bias && j < a.n ? to_f32<T>(static_cast<const T*>(a.ep.bias)[t.group * a.n + j]) : 0.f;
 }
 
-// Tokens [0, t.rows) of a tile that one thread block summed.
-template <typename T, int kChunk>
-__device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part)
+// A tile that needs no sum over a cluster; group e of kGroups takes every
+// kGroups-th chunk, through a `part` of its own.
+template <typename T, int kChunk, int kGroups>
+__device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part, int e)
 {
     constexpr int N = Lanes<T>::kCount, kPer = 128 / N, kItems = kChunk * kPer / 128;
     const int tid = threadIdx.x & 127, line = (threadIdx.x / 32) % 4 * 32 + (threadIdx.x & 31);
@@ -173,7 +191,7 @@ __device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uin
     const bool in = whole && t.feature + lane < a.n;
     const int64_t at0 = (int64_t)(t.row + token0) * a.n + t.feature + lane, step = (int64_t)(128 / kPer) * a.n;
 #pragma unroll 1
-    for (int c0 = 0; c0 < t.rows; c0 += kChunk) {
+    for (int c0 = e * kChunk; c0 < t.rows; c0 += kGroups * kChunk) {
         const int rows = min(kChunk, t.rows - c0);
         const int64_t at = at0 + (int64_t)c0 * a.n;
         Extra x[kItems];
@@ -181,7 +199,7 @@ __device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uin
         for (int k = 0; k < kItems; ++k)
             if (in && token0 + k * (128 / kPer) < rows) x[k] = load_extra<T>(a.ep, at + k * step);
         to_part<true>(acc, c0, rows, part, S, bias, a.ep.act);
-        tile_bar();
+        tile_bar(e);
         if (whole) {
 #pragma unroll
             for (int k = 0; k < kItems; ++k) {
@@ -202,7 +220,7 @@ __device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uin
             for (int c = 0; c < rows; ++c)
                 finish_one<T>(a.ep, part[c * kPartRow + line], (int64_t)(t.row + c0 + c) * a.n + t.feature + line);
         }
-        tile_bar();
+        tile_bar(e);
     }
 }
 
@@ -220,7 +238,7 @@ __device__ __forceinline__ bool write_tile_split(const TileArgs& a, const Tile& 
     bool ok = mbar_wait(empty, parity ^ 1, dead);          // every peer has read the tile before
     if (ok) to_part<false>(acc, 0, t.rows, part, 0.f, 0.f, 0);
     tc_fence_before();
-    tile_bar();
+    tile_bar(0);
     if (tid == 0) mbar_arrive(acc_empty);
     if (tid < a.split) mbar_arrive_peer(full, tid);
     const bool whole = whole_rows<T>(a);
@@ -273,7 +291,7 @@ __device__ __forceinline__ bool write_tile_split(const TileArgs& a, const Tile& 
             finish_one<T>(a.ep, z[0], (int64_t)(t.row + c) * a.n + t.feature + tid);
         }
     }
-    tile_bar();
+    tile_bar(0);
     if (tid < a.split) mbar_arrive_peer(empty, tid);
     return ok;
 }

@@ -157,31 +157,53 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait()
+// Arrival on `bar` (one of its expected ones) when the thread's cp_async4 so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar)
 {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-// Shared memory written by ordinary stores, to be read by the tensor cores or copies.
+// Between shared memory written by threads (cp_async4 too) and its use by the
+// tensor cores or tensor copies: by the writer before it signals, or by the
+// user after it has waited.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ---------------------------------------------------------------- tensor memory
+// G: thread blocks that the tensor-core operations span (2: a cluster's pair,
+// both of which allocate and free; the even one issues everything else).
 // One warp allocates (and later frees) `cols` columns, a power of two from 32.
-__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols)
+template <int G> __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols)
 {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if (G == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
 }
-__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
+template <int G> __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
 {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    if (G == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// Arrival on `bar` when every tensor-core operation this thread issued has completed.
-__device__ __forceinline__ void tc_commit(uint32_t bar)
+// Arrival on `bar` (of both thread blocks of a pair) when every tensor-core
+// operation this thread issued has completed.
+template <int G> __device__ __forceinline__ void tc_commit(uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    if (G == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                bar), "h"((uint16_t)3)
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                     : "memory");
 }
 // 32 lanes x 16 columns of binary32: register i of lane l is column i of the warp's lane l
 // (the wait is part of the statement: nothing may use the registers before it).
@@ -209,21 +231,38 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t addr)
     return (uint64_t)((addr & 0x3FFFF) >> 4) | (1ull << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
 }
 // Scale tile -> 4 columns of tensor memory, repeated for the four lane quarters.
-__device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint64_t desc)
+template <int G> __device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint64_t desc)
 {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+    if (G == 2)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
-// D[128][N] (+)= A[128][64] * B[N][64]^T, E2M1 with block scales in tensor
-// memory: NVFP4 four E4M3 scales per row, MXFP4 two E8M0 ones.
-template <bool MX>
+// D[128 G][N] (+)= A[128 G][64] * B[N][64]^T, E2M1 with block scales in tensor
+// memory: NVFP4 four E4M3 scales per row, MXFP4 two E8M0 ones.  Of a pair,
+// each thread block holds its 128 rows of A and D with their scales, half the
+// rows of B and the scales of all of B.
+template <bool MX, int G>
 __device__ __forceinline__ void tc_mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                            uint32_t sfb, bool add)
 {
-    if (MX)
+    if (MX && G == 2)
         asm volatile(
             "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-                d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)add)
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)add)
+            : "memory");
+    else if (MX)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)add)
+            : "memory");
+    else if (G == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)add)
             : "memory");
     else
         asm volatile(
@@ -233,11 +272,11 @@ __device__ __forceinline__ void tc_mma_fp4(uint32_t d, uint64_t a, uint64_t b, u
             : "memory");
 }
 // Instruction descriptor of tc_mma_fp4: E2M1 operands (format 1), both K-major,
-// 128 x n; scale type E8M0 for MXFP4; `id` the byte of a scale column that the
+// m x n; scale type E8M0 for MXFP4; `id` the byte of a scale column that the
 // operands' first scale is in.
-__device__ __forceinline__ uint32_t idesc_fp4(bool mx, uint32_t n, uint32_t id)
+__device__ __forceinline__ uint32_t idesc_fp4(bool mx, uint32_t m, uint32_t n, uint32_t id)
 {
-    return (id << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((mx ? 1u : 0u) << 23) | ((128u >> 4) << 24) |
+    return (id << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((mx ? 1u : 0u) << 23) | ((m >> 4) << 24) |
            (id << 29);
 }
 
