@@ -157,7 +157,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 if (!(ok = mbar_wait(full + 8 * g.stage, g.parity, dead))) break;
                 fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_peer(peer_full + 8 * g.stage, rank - 1);
+                if (lane == 0) mbar_signal_peer(peer_full + 8 * g.stage, rank - 1);
             }
     } else if (warp == 1) {
         Ring<C::kStages> g, last2;                         // last2 follows two steps behind
@@ -291,7 +291,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 tile_bar(e);
                 if (warp % 4 == 0 && lane == 0) {
                     if (G > 1)
-                        mbar_arrive_peer(acc_empty + 8 * ac.stage, rank & ~1u);
+                        mbar_signal_peer(acc_empty + 8 * ac.stage, rank & ~1u);
                     else
                         mbar_arrive(acc_empty + 8 * ac.stage);
                 }

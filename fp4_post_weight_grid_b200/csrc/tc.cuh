@@ -62,6 +62,17 @@ __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar, uint32_t rank)
         "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar), "r"(rank)
         : "memory");
 }
+// The same without a cluster-wide fence of the thread's ordinary writes (which
+// takes over a thousand clocks under load): for signals about tensor memory,
+// or about shared memory that the tensor cores of its own SM read.
+__device__ __forceinline__ void mbar_signal_peer(uint32_t bar, uint32_t rank)
+{
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %0, %1;\n\t"
+        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar), "r"(rank)
+        : "memory");
+}
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
