@@ -5,8 +5,8 @@
 // in steps of 256 columns, in four roles that meet at mbarriers:
 //   warp 0     copies the codes of both operands (128-byte rows, swizzled) and
 //              the weight's tiled scales into a ring of kStages steps;
-//   warps 2-3  copy the tokens' row-major scales into the tiled layout of the
-//              ring, 4 bytes (one row of a tile) at a time;
+//   warps 2-3  bring the tokens' row-major scales into the tiled layout of the
+//              ring, by way of registers;
 //   warp 1     moves a step's scales to tensor memory and issues four products
 //              of 64 columns;
 //   warps 4..  in groups of four, take the accumulator to y.
@@ -79,7 +79,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         if (lane == 0) {
             dead_word = 0;
             for (int i = 0; i < C::kStages; ++i) {
-                mbar_init(full + 8 * i, 1 + 64);           // the copies, the threads of the token scales
+                mbar_init(full + 8 * i, 1 + 1);            // the copies, the warp of the token scales
                 mbar_init(empty + 8 * i, 1);
                 mbar_init(peer_full + 8 * i, 1);
             }
@@ -155,7 +155,6 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step)
             for (int k = k0; k < k1; ++k, g.next()) {
                 if (!(ok = mbar_wait(full + 8 * g.stage, g.parity, dead))) break;
-                fence_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_signal_peer(peer_full + 8 * g.stage, rank - 1);
             }
@@ -177,7 +176,6 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                     last2.next();
                 }
                 if (!ok) break;
-                fence_async_shared();                      // the token scales
                 tc_fence_after();
                 const uint32_t at = ring0 + g.stage * C::kStage;
                 const uint32_t sf = tmem + C::kAccs * BN + step % 2 * C::kScaleCols;
@@ -214,62 +212,77 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             mbar_drain(drain, 0);
         }
     } else if (warp < 4) {
-        // Token scales: thread i of the 64 takes rows i, i + 64, ...; a row's
-        // scales of one tile are 4 neighbouring bytes, at (r % 32) * 16 +
-        // (r / 32) * 4 of that tile.  Where rows start on 4-byte boundaries
-        // they are copied without passing through registers, and the copies
-        // announce themselves; elsewhere the two words around the 4 bytes are
-        // loaded and shifted.
-        constexpr int kRows = (BN + 63) / 64;
-        const int i0 = threadIdx.x - 64;
+        // Token scales: the two warps take turns with the steps, a lane takes
+        // rows lane, lane + 32, ...  A row's scales of one tile are 4
+        // neighbouring bytes, at (r % 32) * 16 + (r / 32) * 4 of that tile.  A
+        // step's loads are issued when the one before last has been stored, so
+        // that they are on their way while the ring is waited for.  One load a
+        // row where rows start on boundaries of a step's bytes (loads of single
+        // words took four times the L1 lookups, 300 clocks a step of 192 rows).
+        constexpr int kRows = (BN + 31) / 32;
         const int64_t scols = a.k / (MX ? 32 : 16), total = (int64_t)a.m * scols;
-        const bool words = scols % 4 == 0;
-        Ring<C::kStages> g;
-        bool ok = true;
-        for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-            const Tile tl = my_tile(t);
-            for (int k = k0; k < k1; ++k, g.next()) {
-                uint32_t v[kRows][kScaleTiles];
-                const int64_t c0 = (int64_t)k * kScaleTiles * 4;
-                if (!words) {
+        const bool wide = scols % (4 * kScaleTiles) == 0 &&
+                          (reinterpret_cast<uintptr_t>(a.x_scales) & (4 * kScaleTiles - 1)) == 0;
+        uint32_t v[kRows][kScaleTiles];
+        auto load = [&](const Tile& tl, int k) {
+            const int64_t c0 = (int64_t)k * kScaleTiles * 4;
 #pragma unroll
-                    for (int q = 0; q < kRows; ++q)
-#pragma unroll
-                        for (int i = 0; i < kScaleTiles; ++i) {
-                            const int r = i0 + 64 * q;
-                            const int64_t c = c0 + 4 * i;
-                            v[q][i] = 0;
-                            if (r < tl.rows && c < scols) v[q][i] = load_bytes4(a.x_scales, (tl.row + r) * scols + c, total,
-                                                                                 (int)min((int64_t)4, scols - c));
-                        }
-                }
-                if (!(ok = mbar_wait(empty + 8 * g.stage, g.parity ^ 1, dead))) break;
-                uint8_t* xs = ring + g.stage * C::kStage + C::kW + C::kX + C::kWS;
-#pragma unroll
-                for (int q = 0; q < kRows; ++q) {
-                    const int r = i0 + 64 * q;
-                    if (r >= BN) break;
-                    const bool in = r < tl.rows;
-                    const uint8_t* src = a.x_scales + (in ? (tl.row + r) * scols : 0);
-#pragma unroll
-                    for (int i = 0; i < kScaleTiles; ++i) {
-                        uint8_t* dst = xs + (i * C::kTokenTiles + r / 128) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4;
-                        const int64_t c = c0 + 4 * i;
-                        if (words) {
-                            const bool there = in && c < scols;
-                            cp_async4(smem_u32(dst), there ? src + c : a.x_scales, there ? 4 : 0);
-                        } else {
-                            *reinterpret_cast<uint32_t*>(dst) = v[q][i];
-                        }
+            for (int q = 0; q < kRows; ++q) {
+                const int r = lane + 32 * q;
+                const bool in = r < tl.rows;
+                const int64_t at = (tl.row + r) * scols + c0;
+                if (wide) {
+                    if (MX) {
+                        const uint2 u = in ? __ldg(reinterpret_cast<const uint2*>(a.x_scales + at)) : make_uint2(0, 0);
+                        v[q][0] = u.x;
+                        v[q][1] = u.y;
+                    } else {
+                        const uint4 u =
+                            in ? __ldg(reinterpret_cast<const uint4*>(a.x_scales + at)) : make_uint4(0, 0, 0, 0);
+                        v[q][0] = u.x;
+                        v[q][1] = u.y;
+                        v[q][kScaleTiles - 2] = u.z;
+                        v[q][kScaleTiles - 1] = u.w;
                     }
-                }
-                if (words) {
-                    cp_async_arrive(full + 8 * g.stage);
                 } else {
-                    fence_async_shared();
-                    mbar_arrive(full + 8 * g.stage);
+                    load_bytes<kScaleTiles>(a.x_scales, at, total, in ? (int)min(scols - c0, (int64_t)4 * kScaleTiles) : 0,
+                                            v[q]);
                 }
             }
+        };
+        Ring<C::kStages> g;
+        bool ok = true;
+        int64_t t = first_tile;
+        int k = k0;
+        Tile tl;
+        auto next = [&] {                                  // the step after (t, k)
+            g.next();
+            if (++k == k1) {
+                k = k0;
+                t += tile_step;
+                if (t < tiles) tl = my_tile(t);
+            }
+        };
+        if (t < tiles) tl = my_tile(t);
+        if (warp == 3 && t < tiles) next();
+        if (t < tiles) load(tl, k);
+        while (t < tiles) {
+            if (!(ok = mbar_wait(empty + 8 * g.stage, g.parity ^ 1, dead))) break;
+            uint8_t* xs = ring + g.stage * C::kStage + C::kW + C::kX + C::kWS;
+#pragma unroll
+            for (int q = 0; q < kRows; ++q) {
+                const int r = lane + 32 * q;
+                if (r >= BN) break;
+#pragma unroll
+                for (int i = 0; i < kScaleTiles; ++i)
+                    *reinterpret_cast<uint32_t*>(xs + (i * C::kTokenTiles + q / 4) * 512 + lane * 16 + q % 4 * 4) = v[q][i];
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full + 8 * g.stage);
+            next();
+            if (t < tiles) next();
+            if (t < tiles) load(tl, k);
         }
     } else {
         const int e = (warp - 4) / 4;

@@ -99,20 +99,30 @@ __device__ __forceinline__ Tile tile_at(const TileArgs& a, const int* before, in
     return r;
 }
 
-// `count` (1 to 4) bytes from byte `at` of p, which is 4-byte aligned and has
-// `total` bytes, in the low bytes of a word, zeros above.
-__device__ __forceinline__ uint32_t load_bytes4(const uint8_t* p, int64_t at, int64_t total, int count)
+// Bytes [at, at + count) of p, which is 4-byte aligned and has `total` bytes,
+// in order into N words, zeros behind them.
+template <int N>
+__device__ __forceinline__ void load_bytes(const uint8_t* p, int64_t at, int64_t total, int count, uint32_t (&v)[N])
 {
     const int64_t lo = at & ~3ll;
-    uint32_t v;
-    if (lo + 8 <= total) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(p + lo);
-        v = __funnelshift_r(__ldg(w), __ldg(w + 1), 8 * (int)(at - lo));
-    } else {
-        v = 0;
-        for (int b = 0; b < count; ++b) v |= (uint32_t)__ldg(p + at + b) << (8 * b);
+    if (lo + 4 * (N + 1) <= total && count > 0) {
+        uint32_t w[N + 1];
+#pragma unroll
+        for (int i = 0; i <= N; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p + lo) + i);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i] = __funnelshift_r(w[i], w[i + 1], 8 * (int)(at - lo));
+            const int left = count - 4 * i;
+            if (left < 4) v[i] = left > 0 ? v[i] & ((1u << (8 * left)) - 1) : 0;
+        }
+    } else {                                               // the last words of the matrix
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i] = 0;
+            for (int b = 0; b < 4; ++b)
+                if (4 * i + b < count) v[i] |= (uint32_t)__ldg(p + at + 4 * i + b) << (8 * b);
+        }
     }
-    return count < 4 ? v & ((1u << (8 * count)) - 1) : v;
 }
 
 // This thread block's share of a tile's steps.

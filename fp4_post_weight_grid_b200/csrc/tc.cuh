@@ -163,19 +163,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
-// 4 bytes, zeros where `bytes` is 0.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// Arrival on `bar` (one of its expected ones) when the thread's cp_async4 so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-// Between shared memory written by threads (cp_async4 too) and its use by the
-// tensor cores or tensor copies: by the writer before it signals, or by the
-// user after it has waited.
+// Shared memory written by ordinary stores, to be read by the tensor cores or copies.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ---------------------------------------------------------------- tensor memory
