@@ -9,10 +9,10 @@
 // global to shared memory as it is.  Roles of a thread block's warps, meeting
 // at mbarriers:
 //   warp 0     copies codes and scales into a ring (steps of 256 columns);
-//   warp 3     copies x into another (steps of 64 columns, 128-byte rows, swizzled);
-//   warp 1     one thread issues the products, 4 of 16 columns per step of x;
+//   warp 3     copies x into another (sub-steps of 64 columns, 128-byte rows, swizzled);
+//   warp 1     issues the products, 4 of 16 columns per sub-step;
 //   warp 2     the tile table, then idle;
-//   warps 4..  DQ groups of four decode, a step of 64 columns at a time;
+//   warps 4..  in kDq groups of four, decode, a sub-step per group at a time;
 //   the last   in groups of four, take the accumulator to y (product_tile.cuh).
 #include "product_host.cuh"
 
@@ -22,19 +22,21 @@ namespace {
 
 constexpr int kStepCols = 256;             // columns of a step of W: 128 bytes of codes
 constexpr int kSubCols = 64;               // columns of a step of x and of decoded W
-constexpr int kACols = kSubCols / 2;       // columns of tensor memory per decoded step
+constexpr int kSubs = kStepCols / kSubCols;
+constexpr int kACols = kSubCols / 2;       // columns of tensor memory per decoded sub-step
 
 template <int BN> struct Config {
-    static constexpr int kW = 128 * 128, kWStage = kW + 4 * 512, kX = BN * 128;
-    static constexpr int kWStages = BN > 128 ? 3 : BN > 64 ? 5 : BN > 32 ? 7 : 8;
-    static constexpr int kXStages = BN > 64 ? 4 : BN > 32 ? 4 : 8;
+    static constexpr int kW = 128 * 128, kWStage = kW + 4 * 512;
+    static constexpr int kXSubs = BN > 64 ? 1 : 4;                  // sub-steps in a stage of x
+    static constexpr int kXTile = BN * 128, kX = kXSubs * kXTile;
+    static constexpr int kWStages = BN > 128 ? 3 : BN > 64 ? 5 : BN > 32 ? 6 : 7;
+    static constexpr int kXStages = BN > 64 ? 4 : BN > 32 ? 2 : BN > 16 ? 3 : 4;
     static constexpr int kAccs = 2;
     static constexpr int kDq = BN <= 64 ? 4 : 2;                    // groups of four decoding warps
     static constexpr int kEpi = BN > 64 ? 2 : 1;                    // groups of four epilogue warps
     static constexpr int kThreads = (4 + 4 * kDq + 4 * kEpi) * 32;
-    static constexpr int kADepth = 2;                               // decoded steps in tensor memory, per group
-    static constexpr int kASteps = kDq * kADepth;
-    static constexpr int kUsed = kAccs * BN + kASteps * kACols;
+    static constexpr int kADepth = 2;                               // sets of kDq decoded sub-steps
+    static constexpr int kUsed = kAccs * BN + kADepth * kDq * kACols;
     static constexpr int kCols = kUsed <= 256 ? 256 : 512;
     static constexpr bool kSplits = BN <= 64;
     static constexpr int kPart = (kSplits ? BN : 32) * kPartRow * 4;        // sums on their way to y, per group
@@ -160,7 +162,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
 {
     using C = Config<BN>;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t bars[2 * (C::kWStages + C::kXStages + C::kASteps + C::kAccs) + 3];
+    __shared__ __align__(8) uint64_t bars[2 * (C::kWStages + C::kXStages + C::kADepth + C::kAccs) + 3];
     __shared__ int before[FP4Q_PRODUCT_GROUPS_MAX + 1];
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_word, good_offsets;
@@ -171,8 +173,8 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     uint8_t* x_ring = w_ring + C::kWStages * C::kWStage;
     float* part = reinterpret_cast<float*>(x_ring + C::kXStages * C::kX);
     const uint32_t w_full = smem_u32(bars), w_empty = w_full + 8 * C::kWStages, x_full = w_empty + 8 * C::kWStages,
-                   x_empty = x_full + 8 * C::kXStages, a_full = x_empty + 8 * C::kXStages, a_empty = a_full + 8 * C::kASteps,
-                   acc_full = a_empty + 8 * C::kASteps, acc_empty = acc_full + 8 * C::kAccs,
+                   x_empty = x_full + 8 * C::kXStages, a_full = x_empty + 8 * C::kXStages, a_empty = a_full + 8 * C::kADepth,
+                   acc_full = a_empty + 8 * C::kADepth, acc_empty = acc_full + 8 * C::kAccs,
                    part_full = acc_empty + 8 * C::kAccs, part_empty = part_full + 8, drain = part_empty + 8;
     const uint32_t rank = a.split > 1 ? cluster_rank() : 0;
 
@@ -187,8 +189,8 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 mbar_init(x_full + 8 * i, 1);
                 mbar_init(x_empty + 8 * i, 1);
             }
-            for (int i = 0; i < C::kASteps; ++i) {
-                mbar_init(a_full + 8 * i, 4);
+            for (int i = 0; i < C::kADepth; ++i) {
+                mbar_init(a_full + 8 * i, 4 * C::kDq);
                 mbar_init(a_empty + 8 * i, 1);
             }
             for (int i = 0; i < C::kAccs; ++i) {
@@ -220,7 +222,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     int k0, k1;
     split_steps(a, (int)rank, k0, k1);
     // sub-steps of 64 columns of step k
-    auto subs = [&](int k) { return min(kStepCols / kSubCols, (a.k - k * kStepCols + kSubCols - 1) / kSubCols); };
+    auto subs = [&](int k) { return min(kSubs, (a.k - k * kStepCols + kSubCols - 1) / kSubCols); };
 
     if (warp == 0) {
         Ring<C::kWStages> w;
@@ -250,12 +252,17 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
             const Tile tl = tile_at<128>(a, before, t);
             const int c1 = min(a.k, k1 * kStepCols);
-            for (int c = k0 * kStepCols; c < c1; c += kSubCols, x.next()) {
+            for (int c = k0 * kStepCols; c < c1; c += kSubCols * C::kXSubs, x.next()) {
                 if (!(ok = mbar_wait(x_empty + 8 * x.stage, x.parity ^ 1, dead))) break;
                 const uint32_t bar = x_full + 8 * x.stage;
+                const int count = min(C::kXSubs, (c1 - c + kSubCols - 1) / kSubCols);
                 if (elect_one()) {
-                    mbar_expect(bar, a.tokens * 128);
-                    tma_load(smem_u32(x_ring) + x.stage * C::kX, &x_map, c * 2, tl.row, bar);
+                    mbar_expect(bar, count * a.tokens * 128);
+#pragma unroll
+                    for (int i = 0; i < C::kXSubs; ++i)
+                        if (i < count)
+                            tma_load(smem_u32(x_ring) + x.stage * C::kX + i * C::kXTile, &x_map,
+                                     (c + i * kSubCols) * 2, tl.row, bar);
                 }
                 __syncwarp();
             }
@@ -263,7 +270,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         drain_ring(x, x_full, dead);
     } else if (warp == 1) {
         Ring<C::kXStages> x;
-        Ring<C::kADepth> dec[C::kDq];
+        Ring<C::kADepth> d;
         Ring<C::kAccs> ac;
         bool ok = true;
         const uint64_t desc0 = desc_k128(smem_u32(x_ring));
@@ -276,25 +283,27 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             for (int k = k0; ok && k < k1; ++k) {
                 const int count = subs(k);
 #pragma unroll
-                for (int i = 0; i < kStepCols / kSubCols; ++i) {
-                    if (!ok || i >= count) break;
-                    Ring<C::kADepth>& d = dec[i % C::kDq];
-                    const uint32_t as = i % C::kDq * C::kADepth + d.stage;
-                    if (!(ok = mbar_wait(x_full + 8 * x.stage, x.parity, dead) &&
-                               mbar_wait(a_full + 8 * as, d.parity, dead)))
-                        break;
+                for (int i = 0; i < kSubs; ++i) {
+                    if (i >= count) break;
+                    // a stage of x starts, a decoded set starts
+                    if (i % C::kXSubs == 0) ok = ok && mbar_wait(x_full + 8 * x.stage, x.parity, dead);
+                    if (i % C::kDq == 0) ok = ok && mbar_wait(a_full + 8 * d.stage, d.parity, dead);
+                    if (!ok) break;
                     tc_fence_after();
+                    const bool x_ends = i % C::kXSubs == C::kXSubs - 1 || i == count - 1;
+                    const bool a_ends = i % C::kDq == C::kDq - 1 || i == count - 1;
                     if (elect_one()) {
 #pragma unroll
                         for (int c = 0; c < kSubCols / 16; ++c)
-                            tc_mma_bf16(acc, a_tmem + as * kACols + c * 8, desc0 + x.stage * (C::kX >> 4) + c * 2,
-                                        idesc, k > k0 || i > 0 || c > 0);
-                        tc_commit<1>(a_empty + 8 * as);
-                        tc_commit<1>(x_empty + 8 * x.stage);
+                            tc_mma_bf16(acc, a_tmem + (d.stage * C::kDq + i % C::kDq) * kACols + c * 8,
+                                        desc0 + (x.stage * C::kX >> 4) + (i % C::kXSubs * C::kXTile >> 4) + c * 2, idesc,
+                                        k > k0 || i > 0 || c > 0);
+                        if (a_ends) tc_commit<1>(a_empty + 8 * d.stage);
+                        if (x_ends) tc_commit<1>(x_empty + 8 * x.stage);
                     }
                     __syncwarp();
-                    d.next();
-                    x.next();
+                    if (a_ends) d.next();
+                    if (x_ends) x.next();
                 }
             }
             if (elect_one()) tc_commit<1>(acc_full + 8 * ac.stage);
@@ -306,8 +315,9 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         }
     } else if (warp >= 4 && warp < 4 + 4 * C::kDq) {
         const int group = (warp - 4) / 4, quarter = warp % 4, row = quarter * 32 + lane;
-        // A group decodes into stages of its own: where a step has fewer
-        // sub-steps than there are groups, they run on at different paces.
+        // Each group decodes one sub-step of every set, or none of the last one
+        // of a ragged step, and waits and signals either way: a group that
+        // skipped a set could take a later phase of its barriers for this one.
         Ring<C::kWStages> w;
         Ring<C::kADepth> d;
         bool ok = true;
@@ -317,23 +327,26 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 const uint8_t* codes = w_ring + w.stage * C::kWStage + row * 128;
                 const uint8_t* scales = w_ring + w.stage * C::kWStage + C::kW + lane * 16 + quarter * 4;
                 const int n = subs(k);
-                for (int i = group; i < n; i += C::kDq, d.next()) {
-                    const uint4 c0 = *reinterpret_cast<const uint4*>(codes + ((2 * i) ^ (row & 7)) * 16);
-                    const uint4 c1 = *reinterpret_cast<const uint4*>(codes + ((2 * i + 1) ^ (row & 7)) * 16);
-                    const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + (MX ? i / 2 : i) * 512);
-                    const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                for (int i = group; i < (n + C::kDq - 1) / C::kDq * C::kDq; i += C::kDq, d.next()) {
                     uint32_t r[32];
-                    if (MX)
-                        decode_mxfp4(c, sc >> (16 * (i & 1)), r);
-                    else
-                        decode_nvfp4(c, sc, r);
-                    const uint32_t as = group * C::kADepth + d.stage;
-                    if (!(ok = mbar_wait(a_empty + 8 * as, d.parity ^ 1, dead))) break;
-                    tc_fence_after();
-                    tmem_store32(a_tmem + as * kACols + ((uint32_t)quarter << 21), r);
-                    tc_fence_before();
+                    if (i < n) {
+                        const uint4 c0 = *reinterpret_cast<const uint4*>(codes + ((2 * i) ^ (row & 7)) * 16);
+                        const uint4 c1 = *reinterpret_cast<const uint4*>(codes + ((2 * i + 1) ^ (row & 7)) * 16);
+                        const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + (MX ? i / 2 : i) * 512);
+                        const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                        if (MX)
+                            decode_mxfp4(c, sc >> (16 * (i & 1)), r);
+                        else
+                            decode_nvfp4(c, sc, r);
+                    }
+                    if (!(ok = mbar_wait(a_empty + 8 * d.stage, d.parity ^ 1, dead))) break;
+                    if (i < n) {
+                        tc_fence_after();
+                        tmem_store32(a_tmem + (d.stage * C::kDq + group) * kACols + ((uint32_t)quarter << 21), r);
+                        tc_fence_before();
+                    }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(a_full + 8 * as);
+                    if (lane == 0) mbar_arrive(a_full + 8 * d.stage);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(w_empty + 8 * w.stage);
