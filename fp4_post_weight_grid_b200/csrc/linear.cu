@@ -23,14 +23,18 @@ namespace {
 constexpr int kStepCols = 256;             // columns of a step of W: 128 bytes of codes
 constexpr int kSubCols = 64;               // columns of a step of x and of decoded W
 constexpr int kSubs = kStepCols / kSubCols;
+constexpr int kTableBytes = 65536;
 constexpr int kACols = kSubCols / 2;       // columns of tensor memory per decoded sub-step
 
 template <int BN> struct Config {
     static constexpr int kW = 128 * 128, kWStage = kW + 4 * 512;
     static constexpr int kXSubs = BN > 64 ? 1 : 4;                  // sub-steps in a stage of x
     static constexpr int kXTile = BN * 128, kX = kXSubs * kXTile;
-    static constexpr int kWStages = BN > 128 ? 3 : BN > 64 ? 5 : BN > 32 ? 6 : 7;
-    static constexpr int kXStages = BN > 64 ? 4 : BN > 32 ? 2 : BN > 16 ? 3 : 4;
+    // Few tokens: codes decoded by table (see decode8_table), which takes the
+    // second 64 KB of shared memory; x and the sums lie before it, W behind.
+    static constexpr bool kTable = BN <= 32;
+    static constexpr int kWStages = BN > 128 ? 3 : BN > 64 ? 5 : BN > 32 ? 6 : 5;
+    static constexpr int kXStages = BN > 64 ? 4 : BN > 32 ? 2 : BN > 16 ? 2 : 4;
     static constexpr int kAccs = 2;
     static constexpr int kDq = BN <= 64 ? 4 : 2;                    // groups of four decoding warps
     static constexpr int kEpi = BN > 64 ? 2 : 1;                    // groups of four epilogue warps
@@ -40,10 +44,11 @@ template <int BN> struct Config {
     static constexpr int kCols = kUsed <= 256 ? 256 : 512;
     static constexpr bool kSplits = BN <= 64;
     static constexpr int kPart = (kSplits ? BN : 32) * kPartRow * 4;        // sums on their way to y, per group
-    static constexpr int kSmem = kWStages * kWStage + kXStages * kX + kEpi * kPart + 1024;
+    static constexpr int kSmem = kWStages * kWStage + (kTable ? 2 * kTableBytes : kXStages * kX + kEpi * kPart + 1024);
+    static_assert(!kTable || kXStages * kX + kEpi * kPart + 1024 <= kTableBytes - 8192, "room before the table");
     static constexpr int kResident = 1;
     static_assert(kUsed <= 512 && kCols * kResident <= 512, "tensor memory");
-    static_assert(kSmem <= 222 * 1024 && kWStage % 1024 == 0 && kX % 1024 == 0, "shared memory");
+    static_assert(kSmem <= (kTable ? 226 : 222) * 1024 && kWStage % 1024 == 0 && kX % 1024 == 0, "shared memory");
 };
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
@@ -84,35 +89,88 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t scale, uint32_t* ou
     out[3] = decode2<3>(lo, hi, scale);
 }
 
+// The same by table, q itself times its half of `scale`: entry b of 256 holds
+// the pair of code byte b, 32 times in a row, one for the bank of each lane (no
+// conflicts whatever the codes).  Entries are 256 bytes apart and the table
+// starts at a multiple of 65536, so that one permutation puts an address
+// together: bits 15..8 the code byte, the rest `lane_base`.  One operation of
+// the ALU pipe a pair and a load: 64 KB of shared memory, which few tokens
+// leave free, and their products are the ones that wait for the decoding.
+template <int J> __device__ __forceinline__ uint32_t lookup2(uint32_t w, uint32_t lane_base, uint32_t scale)
+{
+    uint32_t v;
+    asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(prmt<4 | J << 4 | 6 << 8 | 7 << 12>(w, lane_base)));
+    return mul_bf16x2(v, scale);
+}
+__device__ __forceinline__ void decode8_table(uint32_t w, uint32_t lane_base, uint32_t scale, uint32_t* out)
+{
+    out[0] = lookup2<0>(w, lane_base, scale);
+    out[1] = lookup2<1>(w, lane_base, scale);
+    out[2] = lookup2<2>(w, lane_base, scale);
+    out[3] = lookup2<3>(w, lane_base, scale);
+}
+// Entry b of the table: the pair of its low and high nibble.
+__device__ __forceinline__ uint32_t table_entry(uint32_t b)
+{
+    uint32_t out[4];
+    decode8(b, 0x7E807E80u, out);                          // * 2^126
+    return out[0];
+}
+
 // 64 columns of one row: 32 bytes of codes, and their scales.
 //
-// NVFP4, four E4M3 bytes: the factors are s * 2^119 (from bits 10..4 of a
-// half, where a byte stands for s * 2^-120, in two exact multiplications); the
-// decoded weight is q * s * 2^-7, in range for every q and s.
-__device__ __forceinline__ void decode_nvfp4(const uint32_t (&c)[8], uint32_t scales, uint32_t (&r)[32])
+// NVFP4, four E4M3 bytes: the decoded weight is q * s * 2^-7, in range for every
+// q and s.  The factors are s * 2^119 for decode8 and s * 2^-7 for the table,
+// from bits 10..4 of a half, where a byte stands for s * 2^-120, in two exact
+// multiplications.
+template <bool TABLE>
+__device__ __forceinline__ void decode_nvfp4(const uint32_t (&c)[8], uint32_t scales, uint32_t lane_base,
+                                             uint32_t (&r)[32])
 {
     const uint32_t s = scales & 0x7F7F7F7Fu;
     uint32_t f[2] = {prmt<0x4140>(s, 0) << 4, prmt<0x4342>(s, 0) << 4};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) f[i] = mul_bf16x2(mul_bf16x2(f[i], 0x7F007F00u), 0x77807780u);      // * 2^127 * 2^112
+    for (int i = 0; i < 2; ++i)
+        f[i] = mul_bf16x2(mul_bf16x2(f[i], 0x7F007F00u), TABLE ? 0x38803880u : 0x77807780u);  // 2^127, 2^-14 or 2^112
     if ((s + 0x01010101u) & 0x80808080u) {                 // a byte 0x7F is a NaN
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (((s >> (8 * i)) & 0x7F) == 0x7F) f[i / 2] |= 0x7FFFu << (16 * (i % 2));
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t both = i % 2 ? prmt<0x3232>(f[i / 2], 0) : prmt<0x1010>(f[i / 2], 0);
-        decode8(c[2 * i], both, r + 8 * i);
-        decode8(c[2 * i + 1], both, r + 8 * i + 4);
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t both = i / 2 % 2 ? prmt<0x3232>(f[i / 4], 0) : prmt<0x1010>(f[i / 4], 0);
+        if (TABLE)
+            decode8_table(c[i], lane_base, both, r + 4 * i);
+        else
+            decode8(c[i], both, r + 4 * i);
     }
 }
-// MXFP4, the two E8M0 bytes in the low half of `scales`: the factors are
-// 2^(b-129+126) up to b = 130, and the decoded weight q * 2^(b-129), which is in
-// range up to b = 254; above 130 what is missing multiplies the result.
-__device__ __forceinline__ void decode_mxfp4(const uint32_t (&c)[8], uint32_t scales, uint32_t (&r)[32])
+// MXFP4, the two E8M0 bytes in the low half of `scales`: the decoded weight is
+// q * 2^(b-129), in range up to b = 254.  decode8 takes 2^(b-129+126), which is up
+// to b = 130; above, what is missing multiplies the result.  The table takes
+// 2^(b-129), which is a normal number from b = 3.
+template <bool TABLE>
+__device__ __forceinline__ void decode_mxfp4(const uint32_t (&c)[8], uint32_t scales, uint32_t lane_base,
+                                             uint32_t (&r)[32])
 {
     const uint32_t b = prmt<0x4140>(scales, 0);
+    if (TABLE) {
+        uint32_t f = b * 128u - 0x01000100u;
+        const uint32_t odd = (b + 0x00010001u) & 0x00FC00FCu;
+        if ((odd & 0xFFFFu) == 0 || odd >> 16 == 0) {      // a byte below 3 (a subnormal factor) or 255 (a NaN)
+            f = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t e = (b >> (16 * i)) & 255;
+                f |= (e == 255 ? 0x7FC0u : e < 3 ? 0x10u << e : (e - 2) << 7) << (16 * i);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            decode8_table(c[i], lane_base, i < 4 ? prmt<0x1010>(f, 0) : prmt<0x3232>(f, 0), r + 4 * i);
+        return;
+    }
     const bool large = ((b + 0x007D007Du) & 0x01000100u) != 0;         // a byte above 130
     const uint32_t f = (large ? __vminu2(b, 0x00820082u) : b) * 128u + 0x3E003E00u;
 #pragma unroll
@@ -169,8 +227,10 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     volatile int* dead = &dead_word;
 
     const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
-    uint8_t* w_ring = raw + (1024 - smem_u32(raw) % 1024) % 1024;
-    uint8_t* x_ring = w_ring + C::kWStages * C::kWStage;
+    uint8_t* aligned = raw + (1024 - smem_u32(raw) % 1024) % 1024;
+    uint8_t* table = raw + (kTableBytes - smem_u32(raw) % kTableBytes);
+    uint8_t* w_ring = C::kTable ? table + kTableBytes : aligned;
+    uint8_t* x_ring = C::kTable ? aligned : w_ring + C::kWStages * C::kWStage;
     float* part = reinterpret_cast<float*>(x_ring + C::kXStages * C::kX);
     const uint32_t w_full = smem_u32(bars), w_empty = w_full + 8 * C::kWStages, x_full = w_empty + 8 * C::kWStages,
                    x_empty = x_full + 8 * C::kXStages, a_full = x_empty + 8 * C::kXStages, a_empty = a_full + 8 * C::kADepth,
@@ -209,6 +269,9 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     } else if (warp == 2) {
         const bool ok = tile_table(a, before);
         if (lane == 0) good_offsets = ok;
+    } else if (C::kTable && warp >= 4) {
+        for (int b = warp - 4; b < 256; b += C::kThreads / 32 - 4)
+            *reinterpret_cast<uint32_t*>(table + 256 * b + 4 * lane) = table_entry(b);
     }
     tc_fence_before();
     __syncthreads();
@@ -318,6 +381,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         // Each group decodes one sub-step of every set, or none of the last one
         // of a ragged step, and waits and signals either way: a group that
         // skipped a set could take a later phase of its barriers for this one.
+        const uint32_t lane_base = smem_u32(table) + 4 * lane;
         Ring<C::kWStages> w;
         Ring<C::kADepth> d;
         bool ok = true;
@@ -335,9 +399,9 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                         const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + (MX ? i / 2 : i) * 512);
                         const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
                         if (MX)
-                            decode_mxfp4(c, sc >> (16 * (i & 1)), r);
+                            decode_mxfp4<C::kTable>(c, sc >> (16 * (i & 1)), lane_base, r);
                         else
-                            decode_nvfp4(c, sc, r);
+                            decode_nvfp4<C::kTable>(c, sc, lane_base, r);
                     }
                     if (!(ok = mbar_wait(a_empty + 8 * d.stage, d.parity ^ 1, dead))) break;
                     if (i < n) {
