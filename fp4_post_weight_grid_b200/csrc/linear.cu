@@ -346,28 +346,37 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             for (int k = k0; ok && k < k1; ++k) {
                 const int count = subs(k);
 #pragma unroll
-                for (int i = 0; i < kSubs; ++i) {
+                for (int i = 0; i < kSubs; i += C::kDq) {  // a decoded set
                     if (i >= count) break;
-                    // a stage of x starts, a decoded set starts
-                    if (i % C::kXSubs == 0) ok = ok && mbar_wait(x_full + 8 * x.stage, x.parity, dead);
-                    if (i % C::kDq == 0) ok = ok && mbar_wait(a_full + 8 * d.stage, d.parity, dead);
-                    if (!ok) break;
+                    Ring<C::kXStages> xs[C::kDq];          // where its sub-steps' x is
+#pragma unroll
+                    for (int q = 0; q < C::kDq; ++q) {
+                        xs[q] = x;
+                        if ((i + q) % C::kXSubs == 0 && i + q < count)
+                            ok = ok && mbar_wait(x_full + 8 * x.stage, x.parity, dead);
+                        if ((i + q) % C::kXSubs == C::kXSubs - 1 && i + q < count) x.next();
+                    }
+                    if (!(ok = ok && mbar_wait(a_full + 8 * d.stage, d.parity, dead))) break;
                     tc_fence_after();
-                    const bool x_ends = i % C::kXSubs == C::kXSubs - 1 || i == count - 1;
-                    const bool a_ends = i % C::kDq == C::kDq - 1 || i == count - 1;
                     if (elect_one()) {
 #pragma unroll
-                        for (int c = 0; c < kSubCols / 16; ++c)
-                            tc_mma_bf16(acc, a_tmem + (d.stage * C::kDq + i % C::kDq) * kACols + c * 8,
-                                        desc0 + (x.stage * C::kX >> 4) + (i % C::kXSubs * C::kXTile >> 4) + c * 2, idesc,
-                                        k > k0 || i > 0 || c > 0);
-                        if (a_ends) tc_commit<1>(a_empty + 8 * d.stage);
-                        if (x_ends) tc_commit<1>(x_empty + 8 * x.stage);
+                        for (int q = 0; q < C::kDq; ++q) {
+                            if (i + q >= count) break;
+                            const uint64_t desc = desc0 + (xs[q].stage * C::kX >> 4) + ((i + q) % C::kXSubs * C::kXTile >> 4);
+                            const uint32_t at = a_tmem + (d.stage * C::kDq + q) * kACols;
+#pragma unroll
+                            for (int c = 0; c < kSubCols / 16; ++c)
+                                tc_mma_bf16(acc, at + c * 8, desc + c * 2, idesc, k > k0 || i + q + c > 0);
+                            if ((i + q) % C::kXSubs == C::kXSubs - 1) tc_commit<1>(x_empty + 8 * xs[q].stage);
+                        }
+                        tc_commit<1>(a_empty + 8 * d.stage);
+                        if (C::kXSubs > 1 && i + C::kDq >= count && count % C::kXSubs != 0)
+                            tc_commit<1>(x_empty + 8 * x.stage);
                     }
                     __syncwarp();
-                    if (a_ends) d.next();
-                    if (x_ends) x.next();
+                    d.next();
                 }
+                if (C::kXSubs > 1 && count % C::kXSubs != 0) x.next();     // a ragged step ends its stage
             }
             if (elect_one()) tc_commit<1>(acc_full + 8 * ac.stage);
             __syncwarp();
@@ -425,7 +434,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             const Tile tl = tile_at<128>(a, before, t);
             const uint32_t acc = tmem + ac.stage * BN;
             const float S = MX ? 4.f : a.w_S[tl.group] * 128.f;        // the decoded weights are scaled down
-            ok = mbar_wait(acc_full + 8 * ac.stage, ac.parity, dead);
+            ok = mbar_wait_long(acc_full + 8 * ac.stage, ac.parity, dead);
             tc_fence_after();
             if (C::kSplits && a.split > 1) {
                 ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, parity, rank, dead,

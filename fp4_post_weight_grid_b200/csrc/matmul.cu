@@ -293,7 +293,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             const Tile tl = my_tile(t);
             const uint32_t acc = tmem + ac.stage * BN;
             const float S = MX ? 1.f : a.w_S[tl.group] * *a.x_S;
-            ok = mbar_wait(acc_full + 8 * ac.stage, ac.parity, dead);
+            ok = mbar_wait_long(acc_full + 8 * ac.stage, ac.parity, dead);
             tc_fence_after();
             if (C::kSplits && a.split > 1) {
                 ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, parity, rank, dead,

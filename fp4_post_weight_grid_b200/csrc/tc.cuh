@@ -103,6 +103,21 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
         }
     }
 }
+// For a long wait (the epilogue's for a tile's sums): looks seldom, so that the
+// waiting warps leave the issue slots to the ones that work.
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* dead)
+{
+    const long long t0 = clock64();
+    while (!mbar_try(bar, parity)) {
+        __nanosleep(64);
+        if (*dead) return false;
+        if (clock64() - t0 > kWaitClocks) {
+            *dead = 1;
+            return false;
+        }
+    }
+    return true;
+}
 // For the end of a dead thread block: the wait for what it has in flight.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity)
 {
