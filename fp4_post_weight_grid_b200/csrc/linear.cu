@@ -466,14 +466,18 @@ static cudaError_t launch_one(const Product& p, TileArgs& a, const TileShape& sh
     cudaError_t e = byte_tile_map(&w_map, p.w, p.n * p.groups, p.k / 2, 128);
     if (e == cudaSuccess) e = byte_tile_map(&x_map, p.x, p.m, p.k * 2, shape.tokens);
     if (e != cudaSuccess) return e;
-    const int per_sm = resident_blocks_per_sm(reinterpret_cast<const void*>(kernel), C::kThreads, C::kSmem);
+    static Residency residency;
+    const int per_sm = product_blocks_per_sm(residency, reinterpret_cast<const void*>(kernel), C::kThreads, C::kSmem);
     return launch_tiles(kernel, w_map, x_map, p, a, shape, 1, per_sm, C::kThreads, C::kSmem, s);
 }
 
 template <bool MX, typename T> static cudaError_t launch_shape(const Product& p, cudaStream_t s)
 {
     TileArgs a = tile_args(p, kStepCols, MX ? 128 : 64);
-    const TileShape shape = tile_shape(p, a.k_steps, 1, Config<16>::kResident);
+    // The tensor core truncates where it adds: after 8192 columns a binary32
+    // result would be off by 3e-6 (a plain binary32 sum by 1.5e-6), after 2048 it
+    // is off by 1e-7.  For bf16 results neither shows.
+    const TileShape shape = tile_shape(p, a.k_steps, 1, p.out_bf16 ? INT32_MAX : 2048 / kStepCols);
     if (shape.tokens <= 16) return launch_one<MX, 16, T>(p, a, shape, s);
     if (shape.tokens <= 32) return launch_one<MX, 32, T>(p, a, shape, s);
     if (shape.tokens <= 64) return launch_one<MX, 64, T>(p, a, shape, s);

@@ -35,7 +35,7 @@ template <int BN> struct Config {
     static constexpr int kW = 128 * 128, kX = BN / kPair * 128;     // bytes of a step
     static constexpr int kWS = 4 * 512, kXS = kTokenTiles * 4 * 512;
     static constexpr int kStage = kW + kX + kWS + kXS;
-    static constexpr int kStages = BN > 32 ? 5 : BN == 32 ? 3 : 4;
+    static constexpr int kStages = BN > 32 ? 5 : 8;
     static constexpr int kAccs = 2;
     // Tensor memory: accumulators, then the scales of the last two steps.
     static constexpr int kScaleCols = 4 * 4 * (1 + kTokenTiles);
@@ -46,7 +46,7 @@ template <int BN> struct Config {
     static constexpr int kPart = (kSplits ? BN : 32) * kPartRow * 4;        // sums on their way to y, per group
     static constexpr int kThreads = (4 + 4 * kEpi) * 32;
     static constexpr int kSmem = kStages * kStage + kEpi * kPart + 1024;
-    static constexpr int kResident = BN <= 32 ? 2 : 1;
+    static constexpr int kResident = 1;
     static_assert(kUsed <= 512 && kCols * kResident <= 512, "tensor memory");
     static_assert(kSmem <= 222 * 1024 && kStage % 1024 == 0, "shared memory");
 };
@@ -330,14 +330,15 @@ static cudaError_t launch_one(const Product& p, TileArgs& a, const TileShape& sh
     cudaError_t e = byte_tile_map(&w_map, p.w, p.n * p.groups, p.k / 2, 128);
     if (e == cudaSuccess) e = byte_tile_map(&x_map, p.x, p.m, p.k / 2, shape.tokens / C::kPair);
     if (e != cudaSuccess) return e;
-    const int per_sm = resident_blocks_per_sm(reinterpret_cast<const void*>(kernel), C::kThreads, C::kSmem);
+    static Residency residency;
+    const int per_sm = product_blocks_per_sm(residency, reinterpret_cast<const void*>(kernel), C::kThreads, C::kSmem);
     return launch_tiles(kernel, w_map, x_map, p, a, shape, C::kPair, per_sm, C::kThreads, C::kSmem, s);
 }
 
 template <bool MX, typename T> static cudaError_t launch_shape(const Product& p, cudaStream_t s)
 {
     TileArgs a = tile_args(p, kStepCols, MX ? 128 : 64);
-    const TileShape shape = tile_shape(p, a.k_steps, 2, Config<16>::kResident);
+    const TileShape shape = tile_shape(p, a.k_steps, 2, INT32_MAX);
     if (shape.tokens <= 16) return launch_one<MX, 16, T>(p, a, shape, s);
     if (shape.tokens <= 32) return launch_one<MX, 32, T>(p, a, shape, s);
     if (shape.tokens <= 64) return launch_one<MX, 64, T>(p, a, shape, s);

@@ -41,6 +41,18 @@ cudaError_t byte_tile_map(CUtensorMap* map, const void* base, int64_t rows, int6
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+int product_blocks_per_sm(Residency& r, const void* kernel, int threads, size_t smem)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return resident_blocks_per_sm(kernel, threads, smem);
+    int n = r.cached[dev].load(std::memory_order_relaxed);
+    if (n <= 0) {
+        n = resident_blocks_per_sm(kernel, threads, smem);
+        r.cached[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 TileArgs tile_args(const Product& p, int step_cols, int scale_tile_cols)
 {
     TileArgs a{};
@@ -63,7 +75,7 @@ TileArgs tile_args(const Product& p, int step_cols, int scale_tile_cols)
     return a;
 }
 
-TileShape tile_shape(const Product& p, int k_steps, int pair, int few_per_sm)
+TileShape tile_shape(const Product& p, int k_steps, int pair, int longest)
 {
     const int64_t rows = p.offsets ? (p.m + p.groups - 1) / p.groups : p.m;       // of a group, on average
     const int64_t busy = p.offsets ? std::min<int64_t>(p.groups, p.m) : 1;
@@ -73,26 +85,35 @@ TileShape tile_shape(const Product& p, int k_steps, int pair, int few_per_sm)
         return busy * ((rows + tokens - 1) / tokens) * ((p.n + features - 1) / features);
     };
     // Rounds of tiles over the SMs times the length of one, whose fixed part
-    // is worth about 16 tokens.
+    // (the weight's tile, decoded or copied) weighs as much as about 160 tokens:
+    // 2048 tokens x 14336 x 4096 took 242, 208 and 201 us in tiles of 128, 160 and
+    // 192, FP4 x FP4 on 4096 tokens 152, 136 and 128 us.
     auto cost = [&](int tokens) {
         const int64_t slots = tokens > 128 ? sms / pair : sms;
-        return (tiles(tokens) + slots - 1) / slots * (tokens + 16);
+        return (tiles(tokens) + slots - 1) / slots * (tokens + 160);
     };
     TileShape t{16, 1};
     while (t.tokens < 128 && t.tokens < rows) t.tokens *= 2;
     if (rows > 128) {
         int64_t best = cost(128);
-        for (int tokens = 192; tokens > 128; tokens -= 32)
+        for (int tokens = 160; tokens <= 192; tokens += 32)
             if (cost(tokens) <= best) {
                 best = cost(tokens);
                 t.tokens = tokens;
             }
     }
-    while (t.tokens > 32 && tiles(t.tokens) < (t.tokens > 128 ? sms / pair : sms)) t.tokens = t.tokens > 128 ? 128 : t.tokens / 2;
-    if (t.tokens <= 64) {
-        const int64_t slots = (int64_t)sms * (t.tokens <= 32 ? few_per_sm : 1);
-        while (t.split < 8 && t.split * 2 <= k_steps && tiles(t.tokens) * t.split * 2 <= slots) t.split *= 2;
-    }
+    // Fewer tokens a tile until every SM has one.
+    while (t.tokens > 32 && tiles(t.tokens) < (t.tokens > 128 ? sms / pair : sms))
+        t.tokens = t.tokens > 128 ? 128 : t.tokens / 2;
+    const bool too_long = k_steps > longest;
+    if (too_long) t.tokens = std::min(t.tokens, 64);
+    if (t.tokens <= 64)
+        // Blocks that would idle share the tiles' steps.  Only while all of
+        // them run at once: the exchange of the partial sums is not hidden, and
+        // one in every round cost 16 x 4096 x 14336 23 us, against 11 us in one.
+        while (t.split < 8 && t.split * 2 <= k_steps &&
+               (tiles(t.tokens) * t.split * 2 <= sms || (too_long && t.split * longest < k_steps)))
+            t.split *= 2;
     return t;
 }
 

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 
 #include "launch.h"
 #include "product.h"
@@ -16,13 +17,19 @@ cudaError_t byte_tile_map(CUtensorMap* map, const void* base, int64_t rows, int6
 // The kernel arguments that do not depend on the tile shape.
 TileArgs tile_args(const Product& p, int step_cols, int scale_tile_cols);
 
+// resident_blocks_per_sm without its lock once it is known for the device.
+struct Residency {
+    std::atomic<int> cached[64];
+};
+int product_blocks_per_sm(Residency& r, const void* kernel, int threads, size_t smem);
+
 struct TileShape {
     int tokens;      // rows of x per tile, a multiple of 16 (of 32 above 128), at most 192
     int split;       // thread blocks that share a tile's K
 };
-// pair: thread blocks that share a tile of more than 128 tokens; few_per_sm:
-// resident thread blocks per SM of the tiles of up to 32 tokens.
-TileShape tile_shape(const Product& p, int k_steps, int pair, int few_per_sm);
+// pair: thread blocks that share a tile of more than 128 tokens; longest: most
+// steps that one accumulator may sum.
+TileShape tile_shape(const Product& p, int k_steps, int pair, int longest);
 
 // One launch over all tiles: as many clusters of thread blocks (`pair` or the
 // shape's split) as are resident at once, or as there are tiles, if fewer, each
