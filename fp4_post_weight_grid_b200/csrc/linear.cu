@@ -257,7 +257,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 mbar_init(acc_full + 8 * i, 1);
                 mbar_init(acc_empty + 8 * i, C::kEpi);
             }
-            mbar_init(part_full, a.split);
+            mbar_init(part_full, 1);
             mbar_init(part_empty, a.split);
             mbar_init(drain, 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -269,13 +269,10 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     } else if (warp == 2) {
         const bool ok = tile_table(a, before);
         if (lane == 0) good_offsets = ok;
-    } else if (C::kTable && warp >= 4) {
-        for (int b = warp - 4; b < 256; b += C::kThreads / 32 - 4)
-            *reinterpret_cast<uint32_t*>(table + 256 * b + 4 * lane) = table_entry(b);
     }
     tc_fence_before();
     __syncthreads();
-    if (a.split > 1) cluster_sync_all();
+    if (a.split > 1) cluster_arrive();         // waited for where a peer's memory is first used
     tc_fence_after();
     const uint32_t tmem = tmem_slot, a_tmem = tmem + C::kAccs * BN;
     const int64_t tiles = good_offsets ? (int64_t)before[a.groups] * a.n_tiles : 0;
@@ -391,6 +388,11 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         // of a ragged step, and waits and signals either way: a group that
         // skipped a set could take a later phase of its barriers for this one.
         const uint32_t lane_base = smem_u32(table) + 4 * lane;
+        if (C::kTable) {                                   // filled while the first copies are on their way
+            for (int b = warp - 4; b < 256; b += 4 * C::kDq)
+                *reinterpret_cast<uint32_t*>(table + 256 * b + 4 * lane) = table_entry(b);
+            asm volatile("bar.sync 7, %0;" ::"n"(4 * C::kDq * 32) : "memory");
+        }
         Ring<C::kWStages> w;
         Ring<C::kADepth> d;
         bool ok = true;
@@ -427,6 +429,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         }
     } else if (warp >= 4 + 4 * C::kDq) {
         const int e = (warp - 4 - 4 * C::kDq) / 4;
+        if (a.split > 1) cluster_wait();
         Ring<C::kAccs> ac;
         uint32_t parity = 0;
         bool ok = true;
@@ -447,12 +450,15 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             }
         }
     }
+    __syncwarp();
+    if (a.split > 1 && warp < 4 + 4 * C::kDq) cluster_wait();
     tc_fence_before();
     __syncthreads();
+    if (a.split > 1) cluster_arrive();
     tc_fence_after();
     if (warp == 1) tmem_free<1>(tmem, C::kCols);
     if (threadIdx.x == 0 && *dead) atomicOr(a.status, FP4Q_FLAG_TIMEOUT);
-    if (a.split > 1) cluster_sync_all();       // a peer may still read this block's partial sums
+    if (a.split > 1) cluster_wait();           // a peer may still send to this block
 }
 
 }  // namespace

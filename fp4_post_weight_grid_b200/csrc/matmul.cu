@@ -87,7 +87,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 mbar_init(acc_full + 8 * i, 1);
                 mbar_init(acc_empty + 8 * i, G * C::kEpi);
             }
-            mbar_init(part_full, a.split);
+            mbar_init(part_full, 1);
             mbar_init(part_empty, a.split);
             mbar_init(drain, 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -102,7 +102,9 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     }
     tc_fence_before();
     __syncthreads();
-    if (cluster) cluster_sync_all();
+    // A pair uses each other's memory from the start, a split tile in its epilogue.
+    if (cluster) cluster_arrive();
+    if (G > 1) cluster_wait();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const int64_t tiles = good_offsets ? (int64_t)before[a.groups] * a.n_tiles : 0;
@@ -286,6 +288,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         }
     } else {
         const int e = (warp - 4) / 4;
+        if (G == 1 && cluster) cluster_wait();
         Ring<C::kAccs> ac;
         uint32_t parity = 0;
         bool ok = true;
@@ -311,9 +314,14 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             }
         }
     }
+    __syncwarp();
+    if (G == 1 && cluster && warp < 4) cluster_wait();
     tc_fence_before();
     __syncthreads();
-    if (cluster) cluster_sync_all();           // a peer may still read this block's shared or tensor memory
+    if (cluster) {                             // a peer may still use this block's shared or tensor memory
+        cluster_arrive();
+        cluster_wait();
+    }
     tc_fence_after();
     if (warp == 1) tmem_free<G>(tmem, C::kCols);
     if (threadIdx.x == 0 && *dead) atomicOr(a.status, FP4Q_FLAG_TIMEOUT);

@@ -97,7 +97,7 @@ TileShape tile_shape(const Product& p, int k_steps, int pair, int longest)
     if (rows > 128) {
         int64_t best = cost(128);
         for (int tokens = 160; tokens <= 192; tokens += 32)
-            if (cost(tokens) <= best) {
+            if (p.offsets || cost(tokens) <= best) {       // groups differ: no use in counting rounds
                 best = cost(tokens);
                 t.tokens = tokens;
             }

@@ -234,40 +234,56 @@ __device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uin
     }
 }
 
-// The same where a cluster split the steps: every thread block leaves its
-// partial sums in shared memory, and each finishes its share of the outputs,
-// adding the partials in rank order (the result does not depend on timing).
-// `full`/`empty`: barriers of `split` arrivals, one from every thread block.
+// The same where a cluster split the steps: every thread block sends its
+// partial sums of token c to block c % split, which adds them in rank order (the
+// result does not depend on timing) and finishes the token.  `full` counts the
+// bytes that arrive here, `empty` has an arrival from every block that sends
+// here: this tile's have been read.  (Fetching the partials from the peers
+// instead took two fences and a round trip more, 1.5 us of a small product.)
 template <typename T>
 __device__ __forceinline__ bool write_tile_split(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part,
                                                  uint32_t full, uint32_t empty, uint32_t parity, uint32_t rank,
                                                  volatile int* dead, uint32_t acc_empty)
 {
     constexpr int N = Lanes<T>::kCount, kPer = 128 / N;
-    const int tid = threadIdx.x & 127;
-    bool ok = mbar_wait(empty, parity ^ 1, dead);          // every peer has read the tile before
-    if (ok) to_part<false>(acc, 0, t.rows, part, 0.f, 0.f, 0);
+    const int tid = threadIdx.x & 127, quarter = (threadIdx.x / 32) % 4, line = quarter * 32 + (threadIdx.x & 31);
+    const int shift = __ffs(a.split) - 1;                  // split is a power of two
+    const int slots = (t.rows + a.split - 1) >> shift;     // tokens of a block, at most
+    const int mine = (t.rows - (int)rank + a.split - 1) >> shift;
+    if (tid == 0) mbar_expect(full, mine * a.split * 512);
+    bool ok = mbar_wait(empty, parity ^ 1, dead);          // the tile before has been read everywhere
+    if (ok)
+#pragma unroll 1
+        for (int c0 = 0; c0 < t.rows; c0 += 16) {
+            uint32_t r[16];
+            tmem_load16(r, acc + ((uint32_t)quarter << 21) + c0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int c = c0 + i;
+                if (c < t.rows)
+                    send_f32(smem_u32(part + ((int)rank * slots + (c >> shift)) * 128 + line), __uint_as_float(r[i]), full,
+                             c & (a.split - 1));
+            }
+        }
     tc_fence_before();
     tile_bar(0);
     if (tid == 0) mbar_arrive(acc_empty);
-    if (tid < a.split) mbar_arrive_peer(full, tid);
     const bool whole = whole_rows<T>(a);
     const int lane = tid % kPer * N;                       // a thread keeps its features
     const bool in = whole && t.feature + lane < a.n;
-    int token = (int)rank * (128 / kPer) + tid / kPer;
-    int64_t at = (int64_t)(t.row + token) * a.n + t.feature + lane;
+    int slot = tid / kPer;
+    auto at = [&](int s) { return (int64_t)(t.row + (s << shift) + (int)rank) * a.n + t.feature + lane; };
     Extra x;
     float bias[N];
-    if (in && token < t.rows) {
-        x = load_extra<T>(a.ep, at);
+    if (in && slot < mine) {
+        x = load_extra<T>(a.ep, at(slot));
 #pragma unroll
         for (int i = 0; i < N; ++i) bias[i] = bias_of<T>(a, t, lane + i);
     }
     ok = mbar_wait(full, parity, dead) && ok;
     if (whole) {
 #pragma unroll 1
-        while (ok && in && token < t.rows) {
-            const uint32_t from = smem_u32(part + token * kPartRow + lane);
+        for (; ok && in && slot < mine; slot += 128 / kPer) {
             float z[N];
 #pragma unroll
             for (int k = 0; k < N; ++k) z[k] = 0.f;
@@ -275,7 +291,7 @@ __device__ __forceinline__ bool write_tile_split(const TileArgs& a, const Tile& 
             for (int q = 0; q < a.split; ++q) {
 #pragma unroll
                 for (int k = 0; k < N; k += 4) {
-                    const float4 f = ld_peer_f32x4(from + 4 * k, q);
+                    const float4 f = *reinterpret_cast<const float4*>(part + (q * slots + slot) * 128 + lane + k);
                     z[k] += f.x;
                     z[k + 1] += f.y;
                     z[k + 2] += f.z;
@@ -285,24 +301,21 @@ __device__ __forceinline__ bool write_tile_split(const TileArgs& a, const Tile& 
 #pragma unroll
             for (int k = 0; k < N; ++k) z[k] = z[k] * S + bias[k];
             activate(z, a.ep.act);
-            finish<T>(a.ep, z, x, at);
-            token += a.split * (128 / kPer);
-            at += (int64_t)a.split * (128 / kPer) * a.n;
-            if (token < t.rows) x = load_extra<T>(a.ep, at);
+            finish<T>(a.ep, z, x, at(slot));
+            if (slot + 128 / kPer < mine) x = load_extra<T>(a.ep, at(slot + 128 / kPer));
         }
     } else if (ok && t.feature + tid < a.n) {
         const float b = bias_of<T>(a, t, tid);
-        for (int c = (int)rank; c < t.rows; c += a.split) {
-            const uint32_t from = smem_u32(part + c * kPartRow + tid);
+        for (int s = 0; s < mine; ++s) {
             float z[1] = {0.f};
-            for (int q = 0; q < a.split; ++q) z[0] += ld_peer_f32(from, q);
+            for (int q = 0; q < a.split; ++q) z[0] += part[(q * slots + s) * 128 + tid];
             z[0] = z[0] * S + b;
             activate(z, a.ep.act);
-            finish_one<T>(a.ep, z[0], (int64_t)(t.row + c) * a.n + t.feature + tid);
+            finish_one<T>(a.ep, z[0], (int64_t)(t.row + (s << shift) + (int)rank) * a.n + t.feature + tid);
         }
     }
     tile_bar(0);
-    if (tid < a.split) mbar_arrive_peer(empty, tid);
+    if (tid < a.split) mbar_signal_peer(empty, tid);
     return ok;
 }
 

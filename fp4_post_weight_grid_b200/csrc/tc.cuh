@@ -53,24 +53,28 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Arrival on the barrier at the same offset in thread block `rank` of the cluster.
-__device__ __forceinline__ void mbar_arrive_peer(uint32_t bar, uint32_t rank)
-{
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\t"
-        "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar), "r"(rank)
-        : "memory");
-}
-// The same without a cluster-wide fence of the thread's ordinary writes (which
-// takes over a thousand clocks under load): for signals about tensor memory,
-// or about shared memory that the tensor cores of its own SM read.
+// Arrival on the barrier at the same offset in thread block `rank` of the
+// cluster.  It does not wait for the thread's ordinary writes to become visible
+// there (a fence that takes over a thousand clocks under load): for signals
+// about tensor memory, about shared memory that the tensor cores of its own SM
+// read, and about data that has been read.
 __device__ __forceinline__ void mbar_signal_peer(uint32_t bar, uint32_t rank)
 {
     asm volatile(
         "{\n\t.reg .b32 a;\n\t"
         "mapa.shared::cluster.u32 a, %0, %1;\n\t"
         "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar), "r"(rank)
+        : "memory");
+}
+// A float to the same offset in thread block `rank`, counted there as 4 bytes on `bar`.
+__device__ __forceinline__ void send_f32(uint32_t addr, float v, uint32_t bar, uint32_t rank)
+{
+    asm volatile(
+        "{\n\t.reg .b32 a, b;\n\t"
+        "mapa.shared::cluster.u32 a, %0, %3;\n\t"
+        "mapa.shared::cluster.u32 b, %2, %3;\n\t"
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [a], %1, [b];\n\t}" ::"r"(addr),
+        "r"(__float_as_uint(v)), "r"(bar), "r"(rank)
         : "memory");
 }
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
@@ -133,30 +137,11 @@ __device__ __forceinline__ uint32_t cluster_rank()
     asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync_all()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float ld_peer_f32(uint32_t addr, uint32_t rank)
-{
-    float v;
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\t"
-        "mapa.shared::cluster.u32 a, %1, %2;\n\t"
-        "ld.shared::cluster.f32 %0, [a];\n\t}"
-        : "=f"(v) : "r"(addr), "r"(rank) : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 ld_peer_f32x4(uint32_t addr, uint32_t rank)
-{
-    float4 v;
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\t"
-        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
-        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
-        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank) : "memory");
-    return v;
-}
+// A barrier of all threads of the cluster that orders no ordinary writes: for
+// what mbarrier initialisations (fenced by themselves) and allocations need, and
+// so that no block ends while a peer uses its memory.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // ---------------------------------------------------------------- copies to shared memory
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map)
