@@ -564,12 +564,15 @@ def fp4q_dequant(fmt: int, codes, scales, d_global_scale, rows: int, cols: int, 
            "fp4q_dequant")
 
 
-def _ptr(t, name, dtype, numel, device):
+def _ptr(t, name, dtype, numel, idx, device):
     """_dev for the products, whose calls are short enough for the checks to
-    count: the same checks, in one comparison while nothing is wrong."""
-    if (type(t) is torch.Tensor and t.dtype is dtype and t.device == device and t.is_contiguous()
-            and (numel is None or t.numel() == numel) and device.type == "cuda"):
-        return t.data_ptr() or None
+    count: the same checks, in one expression while nothing is wrong (`idx` is
+    the index of `device`, -2 where that is no GPU)."""
+    try:
+        if t.dtype is dtype and t.get_device() == idx and t.numel() == numel and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     return _dev(t, name, dtype, numel, device)
 
 
@@ -580,45 +583,51 @@ def _product(name, fmt, x, x_scales, x_global_scale, offsets, w_codes, w_scales,
     if fmt != NVFP4 and fmt != MXFP4:
         raise Fp4qError(ERR_DTYPE, name)
     nv, packed, grouped = fmt == NVFP4, x_scales is not None, offsets is not None
-    block = NVFP4_BLOCK if nv else MXFP4_BLOCK
-    dev, dt, ws, xs, ys = y.device, y.dtype, w_codes.shape, x.shape, y.shape
-    if len(xs) != 2 or len(ys) != 2 or len(ws) != (3 if grouped else 2):
+    dt, ws, xs = y.dtype, w_codes.shape, x.shape
+    if len(xs) != 2 or y.dim() != 2 or len(ws) != (3 if grouped else 2):
         raise ValueError(f"{name}: x and y are 2-D, w_codes {'[groups, n, k/2]' if grouped else '[n, k/2]'}")
-    groups, n, k, m = ws[0] if grouped else 1, ws[-2], 2 * ws[-1], xs[0]
-    if xs[1] != (k // 2 if packed else k) or ys[0] != m or ys[1] != n:
-        raise ValueError(f"{name}: x {tuple(xs)}, w_codes {tuple(ws)} and y {tuple(ys)} do not fit")
+    m, xc = xs
+    if grouped:
+        groups, n, half = ws
+    else:
+        (n, half), groups = ws, 1
+    k = 2 * half
+    if xc != (half if packed else k) or y.shape != (m, n):
+        raise ValueError(f"{name}: x {tuple(xs)}, w_codes {tuple(ws)} and y {tuple(y.shape)} do not fit")
     if k == 0 or k % 32:
         raise Fp4qError(ERR_SHAPE, f"{name}: k = {k} is not a positive multiple of 32")
     if nv and (w_global_scale is None or (packed and x_global_scale is None)):
         raise Fp4qError(ERR_NULL, f"{name}: NVFP4 needs its global scales")
+    dev = y.device
+    idx = y.get_device()
+    if idx < 0:
+        idx = -2
+    mn = m * n
     ep = None
-    if bias is not None or mul is not None or residual is not None or act:
-        ep = ctypes.byref(Epilogue(None if bias is None else _ptr(bias, "bias", dt, groups * n, dev),
-                                   None if mul is None else _ptr(mul, "mul", dt, m * n, dev),
-                                   None if residual is None else _ptr(residual, "residual", dt, m * n, dev), act))
-    yp, code = _ptr(y, "y", dt, None, dev), _wdtype(y)
-    xp = _ptr(x, "x", torch.uint8 if packed else torch.bfloat16, None, dev)
-    wp = _ptr(w_codes, "w_codes", torch.uint8, None, dev)
-    # fp4q_mma_scale_bytes(n, k / block) per group
-    wsp = _ptr(w_scales, "w_scales", torch.uint8, groups * (-(-n // 128)) * (-(-k // (4 * block))) * 512, dev)
-    gp = _ptr(w_global_scale, "w_global_scale", torch.float32, groups, dev) if nv else None
-    sp = _ptr(d_status, "d_status", torch.int32, 1, dev)
+    if act or bias is not None or mul is not None or residual is not None:
+        ep = ctypes.byref(Epilogue(None if bias is None else _ptr(bias, "bias", dt, groups * n, idx, dev),
+                                   None if mul is None else _ptr(mul, "mul", dt, mn, idx, dev),
+                                   None if residual is None else _ptr(residual, "residual", dt, mn, idx, dev), act))
+    blocks = k // (NVFP4_BLOCK if nv else MXFP4_BLOCK)
+    tail = (_ptr(w_codes, "w_codes", torch.uint8, groups * n * half, idx, dev),
+            # fp4q_mma_scale_bytes(n, blocks) per group
+            _ptr(w_scales, "w_scales", torch.uint8, groups * ((n + 127) // 128) * ((blocks + 3) // 4) * 512, idx, dev),
+            _ptr(w_global_scale, "w_global_scale", torch.float32, groups, idx, dev) if nv else None,
+            n, k, ep, _ptr(y, "y", dt, mn, idx, dev), _wdtype(y), _ptr(d_status, "d_status", torch.int32, 1, idx, dev))
     if packed:
-        head = (fmt, xp, _ptr(x_scales, "x_scales", torch.uint8, m * (k // block), dev),
-                _ptr(x_global_scale, "x_global_scale", torch.float32, 1, dev) if nv else None, m)
+        head = (fmt, _ptr(x, "x", torch.uint8, m * half, idx, dev),
+                _ptr(x_scales, "x_scales", torch.uint8, m * blocks, idx, dev),
+                _ptr(x_global_scale, "x_global_scale", torch.float32, 1, idx, dev) if nv else None, m)
     else:
-        head = (fmt, xp, m)
+        head = (fmt, _ptr(x, "x", torch.bfloat16, m * k, idx, dev), m)
     if grouped:
-        head += (_ptr(offsets, "offsets", torch.int32, groups + 1, dev), groups)
-    fn = getattr(load(), name)
-    here = torch.cuda.current_device()
-    if dev.index == here:
-        if stream is None:
-            stream = torch._C._cuda_getCurrentRawStream(here)
-        status = fn(*head, wp, wsp, gp, n, k, ep, yp, code, sp, stream if type(stream) is int else _stream(stream))
+        head += (_ptr(offsets, "offsets", torch.int32, groups + 1, idx, dev), groups)
+    fn = getattr(_lib or load(), name)
+    if torch._C._cuda_getDevice() == idx:
+        status = fn(*head, *tail, torch._C._cuda_getCurrentRawStream(idx) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(dev):
-            status = fn(*head, wp, wsp, gp, n, k, ep, yp, code, sp, _stream(stream))
+            status = fn(*head, *tail, _stream(stream))
     if status:
         raise Fp4qError(status, name)
 

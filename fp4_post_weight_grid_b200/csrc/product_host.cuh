@@ -59,7 +59,7 @@ cudaError_t launch_tiles(Kernel kernel, const CUtensorMap& w_map, const CUtensor
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = blocks > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, w_map, x_map, a);
 }
 

@@ -225,6 +225,15 @@ def test_exact_groups(form, fmt, counts, before, behind, n, k):
 
 
 @pytest.mark.parametrize("form,fmt", FORMS, ids=form_ids)
+@pytest.mark.parametrize("counts,n", [([1, 200], 600), ([0, 0, 0, 330], 300), ([5, 400], 601)])
+def test_exact_groups_whose_tiles_outnumber_the_clusters(form, fmt, counts, n):
+    # few tiles are expected from the average group, so that clusters share K; one group has many
+    p = Problem(form, fmt, 0, n, 2336, counts=counts, behind=1, exact=True, bias=True)
+    p.w_codes &= 0x99
+    p.check(exact=True)
+
+
+@pytest.mark.parametrize("form,fmt", FORMS, ids=form_ids)
 @pytest.mark.parametrize("counts", [[300, 0, 513, 100], [90, 130], [33, 40, 61]])
 def test_exact_groups_of_wide_tiles(form, fmt, counts):
     Problem(form, fmt, 0, 10001, 352, counts=counts, behind=3, exact=True, bias=True).check(exact=True)
