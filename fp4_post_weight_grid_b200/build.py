@@ -18,10 +18,10 @@ ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp4q.so")
 SOURCES = ["api.cu", "absmax.cu", "nvfp4.cu", "mxfp4.cu", "dequant.cu", "batch.cu", "dynamic.cu", "layout.cu", "focus.cu", "gptq.cu",
-           "product.cu", "matmul.cu", "linear.cu"]
+           "product.cu", "matmul.cu", "linear.cu", "few.cu"]
 HEADERS = ["device.cuh", "launch.h", "screen.cuh", "nvfp4_block.cuh", "mxfp4_block.cuh", "batch.h", "wait.cuh",
            "product.h", "product_epilogue.cuh", "tc.cuh", "product_tile.cuh",
-           "product_host.cuh"]
+           "product_host.cuh", "decode.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -14,6 +14,7 @@
 //   warp 2     the tile table, then idle;
 //   warps 4..  in kDq groups of four, decode, a sub-step per group at a time;
 //   the last   in groups of four, take the accumulator to y (product_tile.cuh).
+#include "decode.cuh"
 #include "product_host.cuh"
 
 namespace fp4q {
@@ -51,44 +52,6 @@ template <int BN> struct Config {
     static_assert(kSmem <= (kTable ? 226 : 222) * 1024 && kWStage % 1024 == 0 && kX % 1024 == 0, "shared memory");
 };
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-template <uint32_t kSel> __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "n"(kSel));
-    return r;
-}
-
-// Eight codes -> four pairs of bf16 in column order, each q * 2^-126 times its
-// half of `scale`.  Where bf16 keeps the low exponent bits and the first
-// mantissa bit (8..6), the three magnitude bits of a code are its value under
-// an exponent bias of 127 instead of 1 (the code 1/2 becomes a subnormal,
-// which the multiplication takes exactly); the sign goes to bit 15.  A pair's
-// nibbles come to bits 3..0 of the two halves (the permutation's sign mode
-// gives the zero bytes between them), one integer multiplication by 2^6 + 2^12
-// puts both copies of each in place, and a mask keeps the bits wanted: two
-// operations of the ALU pipe a pair, which is what bounds the decoding, where
-// shifting and merging took four (212 -> 125 ALU instructions per warp and step).
-template <int J> __device__ __forceinline__ uint32_t decode2(uint32_t lo, uint32_t hi, uint32_t scale)
-{
-    const uint32_t p = prmt<J | (J | 8) << 4 | (4 + J) << 8 | (12 + J) << 12>(lo, hi);
-    return mul_bf16x2((p * 0x1040u) & 0x81C081C0u, scale);
-}
-__device__ __forceinline__ void decode8(uint32_t w, uint32_t scale, uint32_t* out)
-{
-    const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
-    out[0] = decode2<0>(lo, hi, scale);
-    out[1] = decode2<1>(lo, hi, scale);
-    out[2] = decode2<2>(lo, hi, scale);
-    out[3] = decode2<3>(lo, hi, scale);
-}
-
 // The same by table, q itself times its half of `scale`: entry b of 256 holds
 // the pair of code byte b, 32 times in a row, one for the bank of each lane (no
 // conflicts whatever the codes).  Entries are 256 bytes apart and the table
@@ -118,71 +81,37 @@ __device__ __forceinline__ uint32_t table_entry(uint32_t b)
 }
 
 // 64 columns of one row: 32 bytes of codes, and their scales.
-//
-// NVFP4, four E4M3 bytes: the decoded weight is q * s * 2^-7, in range for every
-// q and s.  The factors are s * 2^119 for decode8 and s * 2^-7 for the table,
-// from bits 10..4 of a half, where a byte stands for s * 2^-120, in two exact
-// multiplications.
 template <bool TABLE>
 __device__ __forceinline__ void decode_nvfp4(const uint32_t (&c)[8], uint32_t scales, uint32_t lane_base,
                                              uint32_t (&r)[32])
 {
-    const uint32_t s = scales & 0x7F7F7F7Fu;
-    uint32_t f[2] = {prmt<0x4140>(s, 0) << 4, prmt<0x4342>(s, 0) << 4};
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        f[i] = mul_bf16x2(mul_bf16x2(f[i], 0x7F007F00u), TABLE ? 0x38803880u : 0x77807780u);  // 2^127, 2^-14 or 2^112
-    if ((s + 0x01010101u) & 0x80808080u) {                 // a byte 0x7F is a NaN
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (((s >> (8 * i)) & 0x7F) == 0x7F) f[i / 2] |= 0x7FFFu << (16 * (i % 2));
-    }
+    uint32_t f[2];
+    nv_factors<TABLE>(scales, f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint32_t both = i / 2 % 2 ? prmt<0x3232>(f[i / 4], 0) : prmt<0x1010>(f[i / 4], 0);
         if (TABLE)
-            decode8_table(c[i], lane_base, both, r + 4 * i);
+            decode8_table(c[i], lane_base, one_factor(f[i / 4], i / 2 % 2), r + 4 * i);
         else
-            decode8(c[i], both, r + 4 * i);
+            decode8(c[i], one_factor(f[i / 4], i / 2 % 2), r + 4 * i);
     }
 }
-// MXFP4, the two E8M0 bytes in the low half of `scales`: the decoded weight is
-// q * 2^(b-129), in range up to b = 254.  decode8 takes 2^(b-129+126), which is up
-// to b = 130; above, what is missing multiplies the result.  The table takes
-// 2^(b-129), which is a normal number from b = 3.
+// The two E8M0 bytes in the low half of `scales`.
 template <bool TABLE>
 __device__ __forceinline__ void decode_mxfp4(const uint32_t (&c)[8], uint32_t scales, uint32_t lane_base,
                                              uint32_t (&r)[32])
 {
-    const uint32_t b = prmt<0x4140>(scales, 0);
-    if (TABLE) {
-        uint32_t f = b * 128u - 0x01000100u;
-        const uint32_t odd = (b + 0x00010001u) & 0x00FC00FCu;
-        if ((odd & 0xFFFFu) == 0 || odd >> 16 == 0) {      // a byte below 3 (a subnormal factor) or 255 (a NaN)
-            f = 0;
+    uint32_t rest = 0;
+    const uint32_t f = TABLE ? mx_factors_table(scales) : mx_factors(scales, rest);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t e = (b >> (16 * i)) & 255;
-                f |= (e == 255 ? 0x7FC0u : e < 3 ? 0x10u << e : (e - 2) << 7) << (16 * i);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            decode8_table(c[i], lane_base, i < 4 ? prmt<0x1010>(f, 0) : prmt<0x3232>(f, 0), r + 4 * i);
-        return;
+    for (int i = 0; i < 8; ++i) {
+        if (TABLE)
+            decode8_table(c[i], lane_base, one_factor(f, i / 4), r + 4 * i);
+        else
+            decode8(c[i], one_factor(f, i / 4), r + 4 * i);
     }
-    const bool large = ((b + 0x007D007Du) & 0x01000100u) != 0;         // a byte above 130
-    const uint32_t f = (large ? __vminu2(b, 0x00820082u) : b) * 128u + 0x3E003E00u;
+    if (!TABLE && rest) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) decode8(c[i], i < 4 ? prmt<0x1010>(f, 0) : prmt<0x3232>(f, 0), r + 4 * i);
-    if (large) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t e = (b >> (16 * i)) & 255;
-            const uint32_t h = e == 255 ? 0x7FC0u : (max(e, 130u) - 130 + 127) << 7;
-#pragma unroll
-            for (int q = 0; q < 16; ++q) r[16 * i + q] = mul_bf16x2(r[16 * i + q], h | h << 16);
-        }
+        for (int i = 0; i < 32; ++i) r[i] = mul_bf16x2(r[i], one_factor(rest, i / 16));
     }
 }
 

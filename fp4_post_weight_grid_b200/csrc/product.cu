@@ -119,7 +119,8 @@ TileShape tile_shape(const Product& p, int k_steps, int pair, int longest)
 
 cudaError_t launch_product(const Product& p, cudaStream_t s)
 {
-    return p.packed ? launch_matmul(p, s) : launch_linear(p, s);
+    if (p.packed) return launch_matmul(p, s);
+    return few_tokens(p) ? launch_few(p, s) : launch_linear(p, s);
 }
 
 }  // namespace fp4q

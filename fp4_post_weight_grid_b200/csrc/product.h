@@ -32,6 +32,8 @@ struct Product {
 // All checks are done; m, n and groups are positive.
 cudaError_t launch_product(const Product& p, cudaStream_t s);
 cudaError_t launch_linear(const Product& p, cudaStream_t s);      // bf16 x
+bool few_tokens(const Product& p);                                // bf16 x: whether launch_few is the faster one
+cudaError_t launch_few(const Product& p, cudaStream_t s);
 cudaError_t launch_matmul(const Product& p, cudaStream_t s);      // packed x
 
 }  // namespace fp4q
