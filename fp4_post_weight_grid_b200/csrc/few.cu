@@ -1,18 +1,25 @@
-// few.cu -- fp4q_linear and fp4q_linear_group for a few tokens: every weight is
-// read and decoded once for at most 16 tokens, so that the product is bound by
-// the weights' way from memory and, close behind, by their decoding.
+// few.cu -- fp4q_linear for up to 8 tokens on a weight of moderate size, where
+// what counts is how soon the weights are on their way and how little comes
+// after them.
 //
-// A warp takes 16 or 32 rows of W and every 8th stretch of 256 columns: codes
-// go from global memory to registers, are decoded there in the layout of the
-// first operand of mma.sync.m16n8k16, and meet the tokens' values loaded
-// straight from x.  The sum over k may run in any order as long as both
-// operands agree, so thread t of a quad takes columns 64t .. 64t+63 of the
-// stretch: 32 contiguous bytes of codes of each of its rows, one word of scales
-// and 128 contiguous bytes of its token.  Nothing is exchanged before the
-// block's eight partial sums are added in shared memory: no barriers, no
-// staging, and the loads of the next stretch are under way while one is decoded.
-// (The tensor-memory kernel of linear.cu hands every 64 columns from copying to
-// decoding to multiplying warps, and took twice as long for few tokens.)
+// A warp takes 16 rows of W and every ks-th stretch of 256 columns: codes go
+// from global memory to registers, a stretch ahead, are decoded there in the
+// layout of the first operand of mma.sync.m16n8k16, and meet the tokens'
+// values.  The sum over k may run in any order as long as both operands agree,
+// so of every 128 columns thread t of a quad takes 32t .. 32t+31: 16 contiguous
+// bytes of codes of each of its two rows and 64 of its token.  x lies in shared
+// memory, up to 4096 columns at a time, where 16-byte units change places so
+// that the quads' reads meet different banks (read straight from L1, a read
+// touched 32 lines).  The block's warps share x and, ks at a time, the rows,
+// whose partial sums are added at the end; between phases of x they do not wait
+// for one another, where the tensor-memory kernel of linear.cu hands every 64
+// columns from copying to decoding to multiplying warps.
+//
+// Measured (NVFP4, us, here and there): 1024 x 4096, 1 and 8 tokens 4.3 and 5.6
+// against 7.3 and 7.8; 4096 x 4096 6.1 and 7.4 against 9.5; 14336 x 4096 15.4 and
+// 17.2 against 16.7, 4096 x 14336 16.3 and 21.2 against 16.5 and 16.8.  It is
+// bound by instructions (about 240 a warp for 2048 weights, issue slots two
+// thirds busy), as the decoding alone takes 150.
 #include "decode.cuh"
 #include "product_host.cuh"
 
@@ -23,6 +30,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStretch = 256;                  // columns a warp takes at a time
+constexpr int kTokens = 8;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
@@ -33,7 +41,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 bytes that are read once: around L1, which is left to x and the scales.
+// 16 bytes that are read once: around L1.
 __device__ __forceinline__ uint4 ld_once(const uint8_t* p)
 {
     uint4 v;
@@ -41,178 +49,184 @@ __device__ __forceinline__ uint4 ld_once(const uint8_t* p)
         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
+// `bytes` 16, or 0 for zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// The codes and scales of a thread's part of a stretch: rows g and g + 8 of MT
-// tiles of 16.
-template <int MT> struct Part {
-    uint4 codes[MT][2][2];
-    uint32_t scales[MT][2];
+// A thread's codes of a stretch, rows g and g + 8 and two runs of 32 columns,
+// and the words that hold their scales.
+template <bool MX> struct Part {
+    uint4 codes[2][2];
+    uint32_t words[2][2];
+    // `left`: columns from the thread's first one on; past the last one there are zeros.
+    __device__ __forceinline__ void load(const uint8_t* const (&row)[2], const uint8_t* const (&scales)[2], int s, int t,
+                                         int left)
+    {
+        const int64_t tile = MX ? 2 * s : 4 * s + t / 2;
+        if (left >= 160) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    codes[h][e] = ld_once(row[h] + (int64_t)s * (kStretch / 2) + 64 * e);
+                    words[h][e] = __ldg(reinterpret_cast<const uint32_t*>(scales[h] + tile * 512 + (MX ? 512 : 1024) * e));
+                }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const bool in = 128 * e < left;
+                    codes[h][e] = in ? ld_once(row[h] + (int64_t)s * (kStretch / 2) + 64 * e) : make_uint4(0, 0, 0, 0);
+                    words[h][e] =
+                        in ? __ldg(reinterpret_cast<const uint32_t*>(scales[h] + tile * 512 + (MX ? 512 : 1024) * e)) : 0;
+                }
+        }
+    }
+    // The scales of the two runs, side by side.
+    __device__ __forceinline__ uint32_t scales(int h, int t) const
+    {
+        if (MX) return (words[h][0] >> (8 * t) & 255) | (words[h][1] >> (8 * t) & 255) << 8;
+        return (words[h][0] >> (16 * (t & 1)) & 0xFFFF) | words[h][1] >> (16 * (t & 1)) << 16;
+    }
 };
 
-// MT: tiles of 16 rows of W per warp; NT: tiles of 8 tokens.
-template <bool MX, int MT, int NT, typename T>
-__global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant__ TileArgs a,
-                                                          const uint8_t* __restrict__ w,
-                                                          const __nv_bfloat16* __restrict__ x)
+// ODD: some factors want `rest` too (MXFP4 scales above 8).
+template <bool MX, bool ODD>
+__device__ __forceinline__ void multiply(float (&acc)[4], const Part<MX>& p, const uint32_t (&f)[2][2],
+                                         const uint32_t (&rest)[2], uint32_t x, int g, int t)
 {
-    constexpr int kRows = 16 * MT, kTokens = 8 * NT;
-    __shared__ float sums[kWarps][kTokens][kRows + 1];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane / 4, t = lane % 4;
-    const int group = blockIdx.x / a.n_tiles;
-    const int64_t row0 = (int64_t)(blockIdx.x % a.n_tiles) * kRows;
-    int first = 0, last = a.m;
-    if (a.offsets) {
-        bool ok = true;
-        for (int i = threadIdx.x; i < a.groups; i += kThreads) {
-            const int lo = __ldg(a.offsets + i), hi = __ldg(a.offsets + i + 1);
-            ok = ok && lo >= 0 && lo <= hi && hi <= a.m;
-        }
-        first = __ldg(a.offsets + group);
-        last = __ldg(a.offsets + group + 1);
-        if (!__syncthreads_and(ok)) {
-            if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, FP4Q_FLAG_OFFSETS);
-            return;
-        }
-        if (first == last) return;
-    }
-    const float S = MX ? 4.f : a.w_S[group] * 128.f;       // the decoded weights are scaled down
-    const int stretches = (a.k + kStretch - 1) / kStretch;
-    const int per_scale_tile = MX ? 128 : 64;
-
-    // Rows past the last one repeat it; their sums are not used.
-    const uint8_t* rows[MT][2];
-    const uint8_t* scale_rows[MT][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int i = 0; i < 8; ++i) {                          // 8 columns: a word of codes, 16 bytes of x
+        uint32_t b[4];
+        const int unit = (16 * (i / 4) + 4 * t + i % 4) ^ (t >> 1 | (g & 1) << 1);
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
+                     : "r"(x + unit * 16)
+                     : "memory");
+        uint32_t v[2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t j = min(row0 + 16 * mt + 8 * h + g, a.n - 1);
-            rows[mt][h] = w + ((int64_t)group * a.n + j) * (a.k / 2) + t * 32;
-            scale_rows[mt][h] = a.w_scales + group * a.w_scale_stride + j / 128 * a.w_col_tiles * 512 + j % 32 * 16 +
-                                j % 128 / 32 * 4;
-        }
-    // Columns past the last one are zeros in both operands.
-    auto load = [&](Part<MT>& p, int s) {
-        const int k = s * kStretch + 64 * t;
+            const uint4& q = p.codes[h][i / 4];
+            const uint32_t word = i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
+            const int half = MX ? i / 4 : i / 2 % 2;
+            decode8(word, one_factor(f[h][MX ? 0 : i / 4], half), v[h]);
+            if (ODD && rest[h]) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint8_t* c = rows[mt][h] + (int64_t)s * (kStretch / 2);
-                p.codes[mt][h][0] = k < a.k ? ld_once(c) : make_uint4(0, 0, 0, 0);
-                p.codes[mt][h][1] = k + 32 < a.k ? ld_once(c + 16) : make_uint4(0, 0, 0, 0);
-                p.scales[mt][h] =
-                    k < a.k ? __ldg(reinterpret_cast<const uint32_t*>(scale_rows[mt][h] + k / per_scale_tile * 512)) : 0;
+                for (int c = 0; c < 4; ++c) v[h][c] = mul_bf16x2(v[h][c], one_factor(rest[h], half));
             }
-    };
-
-    for (int tok0 = first; tok0 < last; tok0 += kTokens) {
-        float acc[MT][NT][4] = {};
-        const __nv_bfloat16* xs[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) xs[nt] = x + (int64_t)min(tok0 + 8 * nt + g, last - 1) * a.k + 64 * t;
-        Part<MT> cur, next;
-        if (warp < stretches) load(cur, warp);
-        for (int s = warp; s < stretches; s += kWarps) {
-            if (s + kWarps < stretches) load(next, s + kWarps);
-            const int k = s * kStretch + 64 * t;
-            uint32_t f[MT][2][2], rest[MT][2];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    rest[mt][h] = 0;
-                    if (MX)
-                        f[mt][h][0] = f[mt][h][1] = mx_factors(cur.scales[mt][h] >> (16 * (t & 1)), rest[mt][h]);
-                    else
-                        nv_factors<false>(cur.scales[mt][h], f[mt][h]);
-                }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {                  // 8 columns: a word of codes, 16 bytes of x
-                uint4 b[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    b[nt] = k + 32 * (i / 4) < a.k
-                                ? __ldg(reinterpret_cast<const uint4*>(xs[nt] + (int64_t)s * kStretch + 8 * i))
-                                : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    uint32_t v[2][4];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint4& q = cur.codes[mt][h][i / 4];
-                        const uint32_t word = i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
-                        const int half = MX ? i / 4 : i / 2 % 2;
-                        decode8(word, one_factor(f[mt][h][MX ? 0 : i / 4], half), v[h]);
-                        if (MX && rest[mt][h]) {
-#pragma unroll
-                            for (int q2 = 0; q2 < 4; ++q2) v[h][q2] = mul_bf16x2(v[h][q2], one_factor(rest[mt][h], half));
-                        }
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma16816(acc[mt][nt], v[0][0], v[1][0], v[0][1], v[1][1], b[nt].x, b[nt].y);
-                        mma16816(acc[mt][nt], v[0][2], v[1][2], v[0][3], v[1][3], b[nt].z, b[nt].w);
-                    }
-                }
-            }
-            cur = next;
         }
-        // acc[0..3]: (row g, tokens 2t and 2t + 1), (row g + 8, the same)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sums[warp][8 * nt + 2 * t + i % 2][16 * mt + 8 * (i / 2) + g] = acc[mt][nt][i];
-        __syncthreads();
-        for (int i = threadIdx.x; i < kRows * kTokens; i += kThreads) {
-            const int r = i % kRows, c = i / kRows;
-            const int64_t j = row0 + r;
-            if (tok0 + c >= last || j >= a.n) continue;
-            float z[1] = {0.f};
-#pragma unroll
-            for (int q = 0; q < kWarps; ++q) z[0] += sums[q][c][r];
-            z[0] *= S;
-            if (a.ep.bias) z[0] += to_f32<T>(static_cast<const T*>(a.ep.bias)[group * a.n + j]);
-            activate(z, a.ep.act);
-            finish_one<T>(a.ep, z[0], (int64_t)(tok0 + c) * a.n + j);
-        }
-        __syncthreads();
+        mma16816(acc, v[0][0], v[1][0], v[0][1], v[1][1], b[0], b[1]);
+        mma16816(acc, v[0][2], v[1][2], v[0][3], v[1][3], b[2], b[3]);
     }
 }
 
-template <bool MX, int MT, int NT, typename T>
-cudaError_t launch_one(const Product& p, TileArgs& a, cudaStream_t s)
+// ks warps share 16 rows, 8 / ks of which a block has.  `phase`: columns of x in
+// shared memory at a time.
+template <bool MX, typename T>
+__global__ void __launch_bounds__(kThreads, 2)
+few_kernel(const __grid_constant__ TileArgs a, const uint8_t* __restrict__ w, const __nv_bfloat16* __restrict__ x, int ks,
+           int phase)
 {
-    a.n_tiles = (int)((p.n + 16 * MT - 1) / (16 * MT));
-    few_kernel<MX, MT, NT, T><<<(unsigned)((int64_t)a.n_tiles * p.groups), kThreads, 0, s>>>(
-        a, p.w, static_cast<const __nv_bfloat16*>(p.x));
-    return cudaGetLastError();
+    constexpr int kRows = 16;
+    extern __shared__ __align__(128) uint8_t raw[];
+    __shared__ float sums[kWarps][kTokens][kRows + 1];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane / 4, t = lane % 4;
+    const int part = warp % ks, tiles = kWarps / ks;
+    const int64_t block_row = (int64_t)blockIdx.x * (kRows * tiles), row0 = block_row + warp / ks * kRows;
+    const int stretches = (a.k + kStretch - 1) / kStretch;
+    const uint32_t xs = smem_u32(raw), token_bytes = 2 * phase;
+
+    // Rows past the last one repeat it; their sums are not used.
+    const uint8_t* row[2];
+    const uint8_t* scale_row[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t j = min(row0 + 8 * h + g, a.n - 1);
+        row[h] = w + j * (a.k / 2) + 16 * t;
+        scale_row[h] = a.w_scales + j / 128 * a.w_col_tiles * 512 + j % 32 * 16 + j % 128 / 32 * 4;
+    }
+    float acc[4] = {};
+    Part<MX> next;
+    if (part < stretches) next.load(row, scale_row, part, t, a.k - part * kStretch - 32 * t);
+    int s = part;
+    for (int k0 = 0; k0 < a.k; k0 += phase) {
+        const int cols = min(phase, a.k - k0), units = cols / 8;
+        const int padded = (cols + kStretch - 1) / kStretch * (kStretch / 8);      // to whole stretches, by zeros
+        if (k0 > 0) __syncthreads();                       // the phase before has been read
+        // Unit u of a token's 16-byte units goes to u ^ (bit 3 of u, bit 0 of the
+        // token).  What lies where a token is missing goes into sums that are not used.
+        for (int c = 0; c < a.m; ++c)
+            for (int u = threadIdx.x; u < padded; u += kThreads)
+                cp_async16(xs + c * token_bytes + (u ^ (((u >> 3) & 1) | (c & 1) << 1)) * 16,
+                           x + (int64_t)c * a.k + k0 + (u < units ? 8 * u : 0), u < units ? 16 : 0);
+        cp_async_wait_all();
+        __syncthreads();
+        for (; s * kStretch < k0 + cols; s += ks) {
+            const Part<MX> cur = next;
+            if (s + ks < stretches) next.load(row, scale_row, s + ks, t, a.k - (s + ks) * kStretch - 32 * t);
+            uint32_t f[2][2], rest[2] = {0, 0};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (MX)
+                    f[h][0] = f[h][1] = mx_factors(cur.scales(h, t), rest[h]);
+                else
+                    nv_factors<false>(cur.scales(h, t), f[h]);
+            }
+            const uint32_t at = xs + g * token_bytes + (s * kStretch - k0) * 2;
+            if (MX && __any_sync(~0u, (rest[0] | rest[1]) != 0))
+                multiply<MX, true>(acc, cur, f, rest, at, g, t);
+            else
+                multiply<MX, false>(acc, cur, f, rest, at, g, t);
+        }
+    }
+    // acc[0..3]: (row g, tokens 2t and 2t + 1), (row g + 8, the same)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[warp][2 * t + i % 2][8 * (i / 2) + g] = acc[i];
+    __syncthreads();
+    const float S = MX ? 4.f : *a.w_S * 128.f;             // the decoded weights are scaled down
+    for (int i = threadIdx.x; i < kRows * tiles * a.m; i += kThreads) {
+        const int r = i % (kRows * tiles), c = i / (kRows * tiles);
+        const int64_t j = block_row + r;
+        if (j >= a.n) continue;
+        float z[1] = {0.f};
+        for (int q = 0; q < ks; ++q) z[0] += sums[r / kRows * ks + q][c][r % kRows];
+        z[0] *= S;
+        if (a.ep.bias) z[0] += to_f32<T>(static_cast<const T*>(a.ep.bias)[j]);
+        activate(z, a.ep.act);
+        finish_one<T>(a.ep, z[0], (int64_t)c * a.n + j);
+    }
 }
 
-template <bool MX, typename T> cudaError_t launch_shape(const Product& p, cudaStream_t s)
+template <bool MX, typename T> cudaError_t launch_one(const Product& p, cudaStream_t s)
 {
-    TileArgs a = tile_args(p, kStretch, MX ? 128 : 64);
-    const bool two = p.m > 8 * (int64_t)p.groups;
-    // 32 rows a warp halve the reads of x; 16 where 32 would leave less than two blocks for an SM.
-    if ((p.n + 31) / 32 * std::min<int64_t>(p.groups, p.m) >= 2 * sm_count())
-        return two ? launch_one<MX, 2, 2, T>(p, a, s) : launch_one<MX, 2, 1, T>(p, a, s);
-    return two ? launch_one<MX, 1, 2, T>(p, a, s) : launch_one<MX, 1, 1, T>(p, a, s);
+    const TileArgs a = tile_args(p, kStretch, MX ? 128 : 64);
+    constexpr int kMostPhase = 4096;                       // 64 KB
+    const int phase = (int)std::min<int64_t>((p.k + kStretch - 1) / kStretch * kStretch, kMostPhase);
+    // As many warps to a row as leave all blocks resident at once: 4096 rows took
+    // 6.3, 7.2, 11.3 and 19.2 us with 8, 4, 2 and 1, 14336 rows 22.5, 18.0, 16.1 and
+    // 18.0.
+    int ks = 8;
+    while (ks > 1 && (p.n * ks + 127) / 128 > 2 * sm_count()) ks /= 2;
+    static Residency residency;
+    product_blocks_per_sm(residency, reinterpret_cast<const void*>(few_kernel<MX, T>), kThreads,
+                          (size_t)kTokens * kMostPhase * 2);
+    few_kernel<MX, T><<<(unsigned)((p.n * ks + 127) / 128), kThreads, (size_t)kTokens * phase * 2, s>>>(
+        a, p.w, static_cast<const __nv_bfloat16*>(p.x), ks, phase);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-bool few_tokens(const Product& p)
-{
-    return p.offsets ? p.m <= 64 && p.m <= 16 * (int64_t)p.groups : p.m <= 16;
-}
+bool few_tokens(const Product& p) { return !p.offsets && p.m <= kTokens && p.n * p.k <= 1 << 25; }
 
 cudaError_t launch_few(const Product& p, cudaStream_t s)
 {
-    if (p.mx) return p.out_bf16 ? launch_shape<true, __nv_bfloat16>(p, s) : launch_shape<true, float>(p, s);
-    return p.out_bf16 ? launch_shape<false, __nv_bfloat16>(p, s) : launch_shape<false, float>(p, s);
+    if (p.mx) return p.out_bf16 ? launch_one<true, __nv_bfloat16>(p, s) : launch_one<true, float>(p, s);
+    return p.out_bf16 ? launch_one<false, __nv_bfloat16>(p, s) : launch_one<false, float>(p, s);
 }
 
 }  // namespace fp4q
