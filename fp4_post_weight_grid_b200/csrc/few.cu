@@ -15,11 +15,11 @@
 // for one another, where the tensor-memory kernel of linear.cu hands every 64
 // columns from copying to decoding to multiplying warps.
 //
-// Measured (NVFP4, us, here and there): 1024 x 4096, 1 and 8 tokens 4.3 and 5.6
-// against 7.3 and 7.8; 4096 x 4096 6.1 and 7.4 against 9.5; 14336 x 4096 15.4 and
-// 17.2 against 16.7, 4096 x 14336 16.3 and 21.2 against 16.5 and 16.8.  It is
-// bound by instructions (about 240 a warp for 2048 weights, issue slots two
-// thirds busy), as the decoding alone takes 150.
+// Measured (NVFP4, us, here and there): 1024 x 4096, 1 and 8 tokens 3.9 and 5.2
+// against 7.3 and 7.7; 4096 x 4096 5.5 and 6.7 against 9.4; 14336 x 4096 14.2 and
+// 15.7 against 16.6 and 16.8; 4096 x 14336 15.1 and 19.8 against 16.5 and 16.9;
+// 28672 x 8192 47.0 and 50.6 against 47.5.  It is bound by instructions (about
+// 240 a warp for 2048 weights, 150 of them decoding, issue slots two thirds busy).
 #include "decode.cuh"
 #include "product_host.cuh"
 
@@ -221,7 +221,12 @@ template <bool MX, typename T> cudaError_t launch_one(const Product& p, cudaStre
 
 }  // namespace
 
-bool few_tokens(const Product& p) { return !p.offsets && p.m <= kTokens && p.n * p.k <= 1 << 25; }
+// Beyond 2^26 weights the two kernels are as fast as each other; columns over
+// 8192 take so many phases of x that linear.cu's is faster from 5 tokens on.
+bool few_tokens(const Product& p)
+{
+    return !p.offsets && p.m <= (p.k <= 8192 ? kTokens : 4) && p.n * p.k <= 1 << 26;
+}
 
 cudaError_t launch_few(const Product& p, cudaStream_t s)
 {
