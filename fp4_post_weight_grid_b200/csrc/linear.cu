@@ -12,7 +12,7 @@
 //   warp 3     copies x into another (sub-steps of 64 columns, 128-byte rows, swizzled);
 //   warp 1     issues the products, 4 of 16 columns per sub-step;
 //   warp 2     the tile table, then idle;
-//   warps 4..  in kDq groups of four, decode, a sub-step per group at a time;
+//   warps 4..  in four groups of four, decode;
 //   the last   in groups of four, take the accumulator to y (product_tile.cuh).
 #include "decode.cuh"
 #include "product_host.cuh"
@@ -28,20 +28,23 @@ constexpr int kTableBytes = 65536;
 constexpr int kACols = kSubCols / 2;       // columns of tensor memory per decoded sub-step
 
 template <int BN> struct Config {
+    static constexpr int kPair = BN > 128 ? 2 : 1;                  // thread blocks of a tile
     static constexpr int kW = 128 * 128, kWStage = kW + 4 * 512;
     static constexpr int kXSubs = BN > 64 ? 1 : 4;                  // sub-steps in a stage of x
-    static constexpr int kXTile = BN * 128, kX = kXSubs * kXTile;
+    static constexpr int kXTile = BN / kPair * 128, kX = kXSubs * kXTile;
     // Few tokens: codes decoded by table (see decode8_table), which takes the
     // second 64 KB of shared memory; x and the sums lie before it, W behind.
     static constexpr bool kTable = BN <= 32;
-    static constexpr int kWStages = BN > 128 ? 3 : BN > 64 ? 5 : BN > 32 ? 6 : 5;
-    static constexpr int kXStages = BN > 64 ? 4 : BN > 32 ? 2 : BN > 16 ? 2 : 4;
+    static constexpr int kWStages = BN > 64 ? 5 : BN > 32 ? 6 : 5;
+    static constexpr int kXStages = BN > 128 ? 6 : BN > 64 ? 4 : BN > 32 ? 2 : BN > 16 ? 2 : 4;
     static constexpr int kAccs = 2;
-    static constexpr int kDq = BN <= 64 ? 4 : 2;                    // groups of four decoding warps
+    static constexpr int kDq = 4;                                   // groups of four decoding warps
+    static constexpr int kPiece = BN <= 64 ? 64 : 32;               // columns a group decodes at a time
+    static constexpr int kSet = kDq * kPiece / kSubCols;            // decoded sub-steps that are signalled together
     static constexpr int kEpi = BN > 64 ? 2 : 1;                    // groups of four epilogue warps
     static constexpr int kThreads = (4 + 4 * kDq + 4 * kEpi) * 32;
-    static constexpr int kADepth = 2;                               // sets of kDq decoded sub-steps
-    static constexpr int kUsed = kAccs * BN + kADepth * kDq * kACols;
+    static constexpr int kADepth = 2;                               // decoded sets in tensor memory
+    static constexpr int kUsed = kAccs * BN + kADepth * kSet * kACols;
     static constexpr int kCols = kUsed <= 256 ? 256 : 512;
     static constexpr bool kSplits = BN <= 64;
     static constexpr int kPart = (kSplits ? BN : 32) * kPartRow * 4;        // sums on their way to y, per group
@@ -80,56 +83,66 @@ __device__ __forceinline__ uint32_t table_entry(uint32_t b)
     return out[0];
 }
 
-// 64 columns of one row: 32 bytes of codes, and their scales.
-template <bool TABLE>
-__device__ __forceinline__ void decode_nvfp4(const uint32_t (&c)[8], uint32_t scales, uint32_t lane_base,
-                                             uint32_t (&r)[32])
+// 8 W columns of one row (W = 4 or 8), their scales in the low bytes of `scales`.
+template <bool TABLE, int W>
+__device__ __forceinline__ void decode_nvfp4(const uint32_t (&c)[W], uint32_t scales, uint32_t lane_base,
+                                             uint32_t (&v)[4 * W])
 {
     uint32_t f[2];
-    nv_factors<TABLE>(scales, f);
+    nv_factors<TABLE>(W == 4 ? scales & 0xFFFFu : scales, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < W; ++i) {
         if (TABLE)
-            decode8_table(c[i], lane_base, one_factor(f[i / 4], i / 2 % 2), r + 4 * i);
+            decode8_table(c[i], lane_base, one_factor(f[i / 4], i / 2 % 2), v + 4 * i);
         else
-            decode8(c[i], one_factor(f[i / 4], i / 2 % 2), r + 4 * i);
+            decode8(c[i], one_factor(f[i / 4], i / 2 % 2), v + 4 * i);
     }
 }
-// The two E8M0 bytes in the low half of `scales`.
-template <bool TABLE>
-__device__ __forceinline__ void decode_mxfp4(const uint32_t (&c)[8], uint32_t scales, uint32_t lane_base,
-                                             uint32_t (&r)[32])
+template <bool TABLE, int W>
+__device__ __forceinline__ void decode_mxfp4(const uint32_t (&c)[W], uint32_t scales, uint32_t lane_base,
+                                             uint32_t (&v)[4 * W])
 {
+    if (W == 4) scales = (scales & 0xFFu) | 0x7F00u;       // the second byte is not this piece's
     uint32_t rest = 0;
     const uint32_t f = TABLE ? mx_factors_table(scales) : mx_factors(scales, rest);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < W; ++i) {
         if (TABLE)
-            decode8_table(c[i], lane_base, one_factor(f, i / 4), r + 4 * i);
+            decode8_table(c[i], lane_base, one_factor(f, i / 4), v + 4 * i);
         else
-            decode8(c[i], one_factor(f, i / 4), r + 4 * i);
+            decode8(c[i], one_factor(f, i / 4), v + 4 * i);
     }
     if (!TABLE && rest) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) r[i] = mul_bf16x2(r[i], one_factor(rest, i / 16));
+        for (int i = 0; i < 4 * W; ++i) v[i] = mul_bf16x2(v[i], one_factor(rest, i / 16));
     }
 }
 
-// D[128][N] (+)= A[128][16] * B[N][16]^T, bf16, A in tensor memory.
+// D[128 G][N] (+)= A[128 G][16] * B[N][16]^T, bf16, A in tensor memory.  Of a
+// pair, each thread block holds its 128 rows of A and D and half the rows of B.
+template <int G>
 __device__ __forceinline__ void tc_mma_bf16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-        "r"((uint32_t)add)
-        : "memory");
+    if (G == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+            "r"((uint32_t)add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+            "r"((uint32_t)add)
+            : "memory");
 }
-// Binary32 sums (1 << 4) of bf16 operands (1 << 7, 1 << 10), both K-major, 128 x n.
-__device__ __forceinline__ uint32_t idesc_bf16(uint32_t n)
+// Binary32 sums (1 << 4) of bf16 operands (1 << 7, 1 << 10), both K-major, m x n.
+__device__ __forceinline__ uint32_t idesc_bf16(uint32_t m, uint32_t n)
 {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
-__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[32])
+// One row's pairs, a column of tensor memory each; complete on return.
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[32])
 {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -142,14 +155,24 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 template <bool MX, int BN, typename T>
 __global__ void __launch_bounds__(Config<BN>::kThreads, Config<BN>::kResident)
 linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
               const __grid_constant__ TileArgs a)
 {
     using C = Config<BN>;
+    constexpr int G = C::kPair;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t bars[2 * (C::kWStages + C::kXStages + C::kADepth + C::kAccs) + 3];
+    __shared__ __align__(8) uint64_t bars[2 * (C::kWStages + C::kXStages + C::kAccs) + 3 * C::kADepth + 3];
     __shared__ int before[FP4Q_PRODUCT_GROUPS_MAX + 1];
     __shared__ uint32_t tmem_slot;
     __shared__ int dead_word, good_offsets;
@@ -164,8 +187,9 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     const uint32_t w_full = smem_u32(bars), w_empty = w_full + 8 * C::kWStages, x_full = w_empty + 8 * C::kWStages,
                    x_empty = x_full + 8 * C::kXStages, a_full = x_empty + 8 * C::kXStages, a_empty = a_full + 8 * C::kADepth,
                    acc_full = a_empty + 8 * C::kADepth, acc_empty = acc_full + 8 * C::kAccs,
-                   part_full = acc_empty + 8 * C::kAccs, part_empty = part_full + 8, drain = part_empty + 8;
-    const uint32_t rank = a.split > 1 ? cluster_rank() : 0;
+                   peer_full = acc_empty + 8 * C::kAccs, part_full = peer_full + 8 * C::kADepth, part_empty = part_full + 8, drain = part_empty + 8;
+    const bool cluster = G > 1 || a.split > 1;
+    const uint32_t rank = cluster ? cluster_rank() : 0;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -181,10 +205,11 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             for (int i = 0; i < C::kADepth; ++i) {
                 mbar_init(a_full + 8 * i, 4 * C::kDq);
                 mbar_init(a_empty + 8 * i, 1);
+                mbar_init(peer_full + 8 * i, 1);
             }
             for (int i = 0; i < C::kAccs; ++i) {
                 mbar_init(acc_full + 8 * i, 1);
-                mbar_init(acc_empty + 8 * i, C::kEpi);
+                mbar_init(acc_empty + 8 * i, G * C::kEpi);
             }
             mbar_init(part_full, 1);
             mbar_init(part_empty, a.split);
@@ -194,22 +219,33 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             tma_prefetch_desc(&x_map);
         }
     } else if (warp == 1) {
-        tmem_alloc<1>(smem_u32(&tmem_slot), C::kCols);
+        tmem_alloc<G>(smem_u32(&tmem_slot), C::kCols);
     } else if (warp == 2) {
         const bool ok = tile_table(a, before);
         if (lane == 0) good_offsets = ok;
     }
     tc_fence_before();
     __syncthreads();
-    if (a.split > 1) cluster_arrive();         // waited for where a peer's memory is first used
+    // A pair uses each other's memory from the start, a split tile in its epilogue.
+    if (cluster) cluster_arrive();
+    if (G > 1) cluster_wait();
     tc_fence_after();
     const uint32_t tmem = tmem_slot, a_tmem = tmem + C::kAccs * BN;
     const int64_t tiles = good_offsets ? (int64_t)before[a.groups] * a.n_tiles : 0;
     if (!good_offsets && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, FP4Q_FLAG_OFFSETS);
-    const int64_t first_tile = blockIdx.x / a.split, tile_step = gridDim.x / a.split;
+    const int blocks = G > 1 ? G : a.split;                // of a tile
+    const int64_t first_tile = blockIdx.x / blocks, tile_step = gridDim.x / blocks;
     constexpr int kScaleTile = MX ? 128 : 64;              // columns of a scale tile
     int k0, k1;
-    split_steps(a, (int)rank, k0, k1);
+    split_steps(a, G > 1 ? 0 : (int)rank, k0, k1);
+    // The tile with this thread block's features.
+    auto my_tile = [&](int64_t t) {
+        Tile r = tile_at<128 * G>(a, before, t);
+        if (G > 1) r.feature += 128 * rank;
+        return r;
+    };
+    // Tokens of a tile as the tensor core counts them.
+    auto mma_cols = [&](const Tile& t) { return (t.rows + 16 * G - 1) / (16 * G) * (16 * G); };
     // sub-steps of 64 columns of step k
     auto subs = [&](int k) { return min(kSubs, (a.k - k * kStepCols + kSubCols - 1) / kSubCols); };
 
@@ -217,10 +253,10 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         Ring<C::kWStages> w;
         bool ok = true;
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-            const Tile tl = tile_at<128>(a, before, t);
+            const Tile tl = my_tile(t);
             const int wrow = (int)(tl.group * a.n) + tl.feature;
             const uint8_t* ws = a.w_scales + tl.group * a.w_scale_stride +
-                                (int64_t)(tl.feature / 128) * a.w_col_tiles * 512;
+                                min((int64_t)tl.feature, a.n - 1) / 128 * a.w_col_tiles * 512;   // any, past the last feature
             for (int k = k0; k < k1; ++k, w.next()) {
                 if (!(ok = mbar_wait(w_empty + 8 * w.stage, w.parity ^ 1, dead))) break;
                 const uint32_t at = smem_u32(w_ring) + w.stage * C::kWStage, bar = w_full + 8 * w.stage;
@@ -239,24 +275,44 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         Ring<C::kXStages> x;
         bool ok = true;
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-            const Tile tl = tile_at<128>(a, before, t);
+            const Tile tl = my_tile(t);
             const int c1 = min(a.k, k1 * kStepCols);
+            const int xrow = tl.row + (G > 1 ? (int)rank * (mma_cols(tl) / G) : 0);
             for (int c = k0 * kStepCols; c < c1; c += kSubCols * C::kXSubs, x.next()) {
                 if (!(ok = mbar_wait(x_empty + 8 * x.stage, x.parity ^ 1, dead))) break;
                 const uint32_t bar = x_full + 8 * x.stage;
                 const int count = min(C::kXSubs, (c1 - c + kSubCols - 1) / kSubCols);
                 if (elect_one()) {
-                    mbar_expect(bar, count * a.tokens * 128);
+                    mbar_expect(bar, count * (a.tokens / G) * 128);
 #pragma unroll
                     for (int i = 0; i < C::kXSubs; ++i)
                         if (i < count)
                             tma_load(smem_u32(x_ring) + x.stage * C::kX + i * C::kXTile, &x_map,
-                                     (c + i * kSubCols) * 2, tl.row, bar);
+                                     (c + i * kSubCols) * 2, xrow, bar);
                 }
                 __syncwarp();
             }
         }
         drain_ring(x, x_full, dead);
+    } else if (warp == 1 && rank % G != 0) {
+        // The odd block of a pair tells the even one, which issues for both,
+        // that its half of a set and of its x is there.
+        Ring<C::kXStages> x;
+        Ring<C::kADepth> d;
+        bool ok = true;
+        for (int64_t t = first_tile; ok && t < tiles; t += tile_step)
+            for (int k = k0; ok && k < k1; ++k) {
+                const int count = subs(k);
+                for (int i = 0; ok && i < count; i += C::kSet, d.next()) {
+                    for (int q = 0; q < C::kSet && i + q < count; ++q, x.next())
+                        ok = ok && mbar_wait(x_full + 8 * x.stage, x.parity, dead);
+                    ok = ok && mbar_wait(a_full + 8 * d.stage, d.parity, dead);
+                    tc_fence_after();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_signal_peer(peer_full + 8 * d.stage, rank - 1);
+                }
+            }
     } else if (warp == 1) {
         Ring<C::kXStages> x;
         Ring<C::kADepth> d;
@@ -264,58 +320,62 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         bool ok = true;
         const uint64_t desc0 = desc_k128(smem_u32(x_ring));
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next()) {
-            const Tile tl = tile_at<128>(a, before, t);
-            const uint32_t idesc = idesc_bf16(min(BN, (tl.rows + 15) / 16 * 16));
+            const Tile tl = my_tile(t);
+            const uint32_t idesc = idesc_bf16(128 * G, mma_cols(tl));
             const uint32_t acc = tmem + ac.stage * BN;
             if (!(ok = mbar_wait(acc_empty + 8 * ac.stage, ac.parity ^ 1, dead))) break;
             tc_fence_after();
             for (int k = k0; ok && k < k1; ++k) {
                 const int count = subs(k);
 #pragma unroll
-                for (int i = 0; i < kSubs; i += C::kDq) {  // a decoded set
+                for (int i = 0; i < kSubs; i += C::kSet) {  // a decoded set
                     if (i >= count) break;
-                    Ring<C::kXStages> xs[C::kDq];          // where its sub-steps' x is
+                    Ring<C::kXStages> xs[C::kSet];          // where its sub-steps' x is
 #pragma unroll
-                    for (int q = 0; q < C::kDq; ++q) {
+                    for (int q = 0; q < C::kSet; ++q) {
                         xs[q] = x;
                         if ((i + q) % C::kXSubs == 0 && i + q < count)
                             ok = ok && mbar_wait(x_full + 8 * x.stage, x.parity, dead);
                         if ((i + q) % C::kXSubs == C::kXSubs - 1 && i + q < count) x.next();
                     }
-                    if (!(ok = ok && mbar_wait(a_full + 8 * d.stage, d.parity, dead))) break;
+                    ok = ok && mbar_wait(a_full + 8 * d.stage, d.parity, dead);
+                    if (G > 1) ok = ok && mbar_wait(peer_full + 8 * d.stage, d.parity, dead);
+                    if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
-                        for (int q = 0; q < C::kDq; ++q) {
+                        for (int q = 0; q < C::kSet; ++q) {
                             if (i + q >= count) break;
                             const uint64_t desc = desc0 + (xs[q].stage * C::kX >> 4) + ((i + q) % C::kXSubs * C::kXTile >> 4);
-                            const uint32_t at = a_tmem + (d.stage * C::kDq + q) * kACols;
+                            const uint32_t at = a_tmem + (d.stage * C::kSet + q) * kACols;
 #pragma unroll
                             for (int c = 0; c < kSubCols / 16; ++c)
-                                tc_mma_bf16(acc, at + c * 8, desc + c * 2, idesc, k > k0 || i + q + c > 0);
-                            if ((i + q) % C::kXSubs == C::kXSubs - 1) tc_commit<1>(x_empty + 8 * xs[q].stage);
+                                tc_mma_bf16<G>(acc, at + c * 8, desc + c * 2, idesc, k > k0 || i + q + c > 0);
+                            if ((i + q) % C::kXSubs == C::kXSubs - 1) tc_commit<G>(x_empty + 8 * xs[q].stage);
                         }
-                        tc_commit<1>(a_empty + 8 * d.stage);
-                        if (C::kXSubs > 1 && i + C::kDq >= count && count % C::kXSubs != 0)
-                            tc_commit<1>(x_empty + 8 * x.stage);
+                        tc_commit<G>(a_empty + 8 * d.stage);
+                        if (C::kXSubs > 1 && i + C::kSet >= count && count % C::kXSubs != 0)
+                            tc_commit<G>(x_empty + 8 * x.stage);
                     }
                     __syncwarp();
                     d.next();
                 }
                 if (C::kXSubs > 1 && count % C::kXSubs != 0) x.next();     // a ragged step ends its stage
             }
-            if (elect_one()) tc_commit<1>(acc_full + 8 * ac.stage);
+            if (elect_one()) tc_commit<G>(acc_full + 8 * ac.stage);
             __syncwarp();
         }
         if (*dead) {
-            if (elect_one()) tc_commit<1>(drain);
+            if (elect_one()) tc_commit<G>(drain);
             mbar_drain(drain, 0);
         }
     } else if (warp >= 4 && warp < 4 + 4 * C::kDq) {
         const int group = (warp - 4) / 4, quarter = warp % 4, row = quarter * 32 + lane;
-        // Each group decodes one sub-step of every set, or none of the last one
-        // of a ragged step, and waits and signals either way: a group that
-        // skipped a set could take a later phase of its barriers for this one.
+        // Each group decodes one piece of every set, or none of the last one of a
+        // ragged step, and waits and signals either way: a group that skipped a
+        // set could take a later phase of its barriers for this one.  (Many
+        // tokens: two groups with 64 columns each took 1150 clocks a set, whose
+        // products take 770.)
         const uint32_t lane_base = smem_u32(table) + 4 * lane;
         if (C::kTable) {                                   // filled while the first copies are on their way
             for (int b = warp - 4; b < 256; b += 4 * C::kDq)
@@ -331,22 +391,33 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 const uint8_t* codes = w_ring + w.stage * C::kWStage + row * 128;
                 const uint8_t* scales = w_ring + w.stage * C::kWStage + C::kW + lane * 16 + quarter * 4;
                 const int n = subs(k);
-                for (int i = group; i < (n + C::kDq - 1) / C::kDq * C::kDq; i += C::kDq, d.next()) {
-                    uint32_t r[32];
-                    if (i < n) {
-                        const uint4 c0 = *reinterpret_cast<const uint4*>(codes + ((2 * i) ^ (row & 7)) * 16);
-                        const uint4 c1 = *reinterpret_cast<const uint4*>(codes + ((2 * i + 1) ^ (row & 7)) * 16);
-                        const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + (MX ? i / 2 : i) * 512);
-                        const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                for (int i = 0; i < n; i += C::kSet, d.next()) {
+                    constexpr int kWords = C::kPiece / 8;
+                    const int p = i * (kSubCols / C::kPiece) + group;            // piece of the step
+                    const bool live = p * C::kPiece < n * kSubCols;
+                    uint32_t v[C::kPiece / 2];
+                    if (live) {
+                        uint32_t c[kWords];
+#pragma unroll
+                        for (int q = 0; q < kWords / 4; ++q) {
+                            const uint4 u =
+                                *reinterpret_cast<const uint4*>(codes + ((p * (kWords / 4) + q) ^ (row & 7)) * 16);
+                            c[4 * q] = u.x, c[4 * q + 1] = u.y, c[4 * q + 2] = u.z, c[4 * q + 3] = u.w;
+                        }
+                        // scale bytes of the piece: kPiece / 16 or / 32, of 4 a tile
+                        constexpr int kBytes = C::kPiece / (MX ? 32 : 16), kPer = 4 / kBytes;
+                        const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + p / kPer * 512) >>
+                                            (8 * kBytes * (p % kPer));
                         if (MX)
-                            decode_mxfp4<C::kTable>(c, sc >> (16 * (i & 1)), lane_base, r);
+                            decode_mxfp4<C::kTable>(c, sc, lane_base, v);
                         else
-                            decode_nvfp4<C::kTable>(c, sc, lane_base, r);
+                            decode_nvfp4<C::kTable>(c, sc, lane_base, v);
                     }
                     if (!(ok = mbar_wait(a_empty + 8 * d.stage, d.parity ^ 1, dead))) break;
-                    if (i < n) {
+                    if (live) {
                         tc_fence_after();
-                        tmem_store32(a_tmem + (d.stage * C::kDq + group) * kACols + ((uint32_t)quarter << 21), r);
+                        tmem_store(a_tmem + d.stage * (C::kSet * kACols) + group * (C::kPiece / 2) +
+                                       ((uint32_t)quarter << 21), v);
                         tc_fence_before();
                     }
                     __syncwarp();
@@ -358,12 +429,12 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         }
     } else if (warp >= 4 + 4 * C::kDq) {
         const int e = (warp - 4 - 4 * C::kDq) / 4;
-        if (a.split > 1) cluster_wait();
+        if (G == 1 && cluster) cluster_wait();
         Ring<C::kAccs> ac;
         uint32_t parity = 0;
         bool ok = true;
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next(), parity ^= 1) {
-            const Tile tl = tile_at<128>(a, before, t);
+            const Tile tl = my_tile(t);
             const uint32_t acc = tmem + ac.stage * BN;
             const float S = MX ? 4.f : a.w_S[tl.group] * 128.f;        // the decoded weights are scaled down
             ok = mbar_wait_long(acc_full + 8 * ac.stage, ac.parity, dead);
@@ -375,19 +446,26 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 if (ok) write_tile<T, Chunk<T, BN>::kTokens, C::kEpi>(a, tl, acc, S, part + e * (C::kPart / 4), e);
                 tc_fence_before();
                 tile_bar(e);
-                if (warp % 4 == 0 && lane == 0) mbar_arrive(acc_empty + 8 * ac.stage);
+                if (warp % 4 == 0 && lane == 0) {
+                    if (G > 1)
+                        mbar_signal_peer(acc_empty + 8 * ac.stage, rank & ~1u);
+                    else
+                        mbar_arrive(acc_empty + 8 * ac.stage);
+                }
             }
         }
     }
     __syncwarp();
-    if (a.split > 1 && warp < 4 + 4 * C::kDq) cluster_wait();
+    if (G == 1 && cluster && warp < 4 + 4 * C::kDq) cluster_wait();
     tc_fence_before();
     __syncthreads();
-    if (a.split > 1) cluster_arrive();
+    if (cluster) {                             // a peer may still use this block's shared or tensor memory
+        cluster_arrive();
+        cluster_wait();
+    }
     tc_fence_after();
-    if (warp == 1) tmem_free<1>(tmem, C::kCols);
+    if (warp == 1) tmem_free<G>(tmem, C::kCols);
     if (threadIdx.x == 0 && *dead) atomicOr(a.status, FP4Q_FLAG_TIMEOUT);
-    if (a.split > 1) cluster_wait();           // a peer may still send to this block
 }
 
 }  // namespace
@@ -399,11 +477,11 @@ static cudaError_t launch_one(const Product& p, TileArgs& a, const TileShape& sh
     auto kernel = linear_kernel<MX, BN, T>;
     CUtensorMap w_map, x_map;
     cudaError_t e = byte_tile_map(&w_map, p.w, p.n * p.groups, p.k / 2, 128);
-    if (e == cudaSuccess) e = byte_tile_map(&x_map, p.x, p.m, p.k * 2, shape.tokens);
+    if (e == cudaSuccess) e = byte_tile_map(&x_map, p.x, p.m, p.k * 2, shape.tokens / C::kPair);
     if (e != cudaSuccess) return e;
     static Residency residency;
     const int per_sm = product_blocks_per_sm(residency, reinterpret_cast<const void*>(kernel), C::kThreads, C::kSmem);
-    return launch_tiles(kernel, w_map, x_map, p, a, shape, 1, per_sm, C::kThreads, C::kSmem, s);
+    return launch_tiles(kernel, w_map, x_map, p, a, shape, C::kPair, per_sm, C::kThreads, C::kSmem, s);
 }
 
 template <bool MX, typename T> static cudaError_t launch_shape(const Product& p, cudaStream_t s)
@@ -412,7 +490,7 @@ template <bool MX, typename T> static cudaError_t launch_shape(const Product& p,
     // The tensor core truncates where it adds: after 8192 columns a binary32
     // result would be off by 3e-6 (a plain binary32 sum by 1.5e-6), after 2048 it
     // is off by 1e-7.  For bf16 results neither shows.
-    const TileShape shape = tile_shape(p, a.k_steps, 1, p.out_bf16 ? INT32_MAX : 2048 / kStepCols);
+    const TileShape shape = tile_shape(p, a.k_steps, 2, p.out_bf16 ? INT32_MAX : 2048 / kStepCols);
     if (shape.tokens <= 16) return launch_one<MX, 16, T>(p, a, shape, s);
     if (shape.tokens <= 32) return launch_one<MX, 32, T>(p, a, shape, s);
     if (shape.tokens <= 64) return launch_one<MX, 64, T>(p, a, shape, s);
