@@ -12,7 +12,7 @@
 //   warp 3     copies x into another (sub-steps of 64 columns, 128-byte rows, swizzled);
 //   warp 1     issues the products, 4 of 16 columns per sub-step;
 //   warp 2     the tile table, then idle;
-//   warps 4..  in four groups of four, decode;
+//   warps 4..  in kDq groups of four, decode, a sub-step per group at a time;
 //   the last   in groups of four, take the accumulator to y (product_tile.cuh).
 #include "decode.cuh"
 #include "product_host.cuh"
@@ -38,13 +38,11 @@ template <int BN> struct Config {
     static constexpr int kWStages = BN > 64 ? 5 : BN > 32 ? 6 : 5;
     static constexpr int kXStages = BN > 128 ? 6 : BN > 64 ? 4 : BN > 32 ? 2 : BN > 16 ? 2 : 4;
     static constexpr int kAccs = 2;
-    static constexpr int kDq = 4;                                   // groups of four decoding warps
-    static constexpr int kPiece = BN <= 64 ? 64 : 32;               // columns a group decodes at a time
-    static constexpr int kSet = kDq * kPiece / kSubCols;            // decoded sub-steps that are signalled together
+    static constexpr int kDq = BN <= 64 ? 4 : 2;                    // groups of four decoding warps
     static constexpr int kEpi = BN > 64 ? 2 : 1;                    // groups of four epilogue warps
     static constexpr int kThreads = (4 + 4 * kDq + 4 * kEpi) * 32;
     static constexpr int kADepth = 2;                               // decoded sets in tensor memory
-    static constexpr int kUsed = kAccs * BN + kADepth * kSet * kACols;
+    static constexpr int kUsed = kAccs * BN + kADepth * kDq * kACols;
     static constexpr int kCols = kUsed <= 256 ? 256 : 512;
     static constexpr bool kSplits = BN <= 64;
     static constexpr int kPart = (kSplits ? BN : 32) * kPartRow * 4;        // sums on their way to y, per group
@@ -83,30 +81,30 @@ __device__ __forceinline__ uint32_t table_entry(uint32_t b)
     return out[0];
 }
 
-// 8 W columns of one row (W = 4 or 8), their scales in the low bytes of `scales`.
-template <bool TABLE, int W>
-__device__ __forceinline__ void decode_nvfp4(const uint32_t (&c)[W], uint32_t scales, uint32_t lane_base,
-                                             uint32_t (&v)[4 * W])
+// 64 columns of one row: 32 bytes of codes, and their scales.
+template <bool TABLE>
+__device__ __forceinline__ void decode_nvfp4(const uint32_t (&c)[8], uint32_t scales, uint32_t lane_base,
+                                             uint32_t (&v)[32])
 {
     uint32_t f[2];
-    nv_factors<TABLE>(W == 4 ? scales & 0xFFFFu : scales, f);
+    nv_factors<TABLE>(scales, f);
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
+    for (int i = 0; i < 8; ++i) {
         if (TABLE)
             decode8_table(c[i], lane_base, one_factor(f[i / 4], i / 2 % 2), v + 4 * i);
         else
             decode8(c[i], one_factor(f[i / 4], i / 2 % 2), v + 4 * i);
     }
 }
-template <bool TABLE, int W>
-__device__ __forceinline__ void decode_mxfp4(const uint32_t (&c)[W], uint32_t scales, uint32_t lane_base,
-                                             uint32_t (&v)[4 * W])
+// The two E8M0 bytes in the low half of `scales`.
+template <bool TABLE>
+__device__ __forceinline__ void decode_mxfp4(const uint32_t (&c)[8], uint32_t scales, uint32_t lane_base,
+                                             uint32_t (&v)[32])
 {
-    if (W == 4) scales = (scales & 0xFFu) | 0x7F00u;       // the second byte is not this piece's
     uint32_t rest = 0;
     const uint32_t f = TABLE ? mx_factors_table(scales) : mx_factors(scales, rest);
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
+    for (int i = 0; i < 8; ++i) {
         if (TABLE)
             decode8_table(c[i], lane_base, one_factor(f, i / 4), v + 4 * i);
         else
@@ -114,7 +112,7 @@ __device__ __forceinline__ void decode_mxfp4(const uint32_t (&c)[W], uint32_t sc
     }
     if (!TABLE && rest) {
 #pragma unroll
-        for (int i = 0; i < 4 * W; ++i) v[i] = mul_bf16x2(v[i], one_factor(rest, i / 16));
+        for (int i = 0; i < 32; ++i) v[i] = mul_bf16x2(v[i], one_factor(rest, i / 16));
     }
 }
 
@@ -152,15 +150,6 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[32
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
-        "tcgen05.wait::st.sync.aligned;" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 
@@ -303,8 +292,8 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step)
             for (int k = k0; ok && k < k1; ++k) {
                 const int count = subs(k);
-                for (int i = 0; ok && i < count; i += C::kSet, d.next()) {
-                    for (int q = 0; q < C::kSet && i + q < count; ++q, x.next())
+                for (int i = 0; ok && i < count; i += C::kDq, d.next()) {
+                    for (int q = 0; q < C::kDq && i + q < count; ++q, x.next())
                         ok = ok && mbar_wait(x_full + 8 * x.stage, x.parity, dead);
                     ok = ok && mbar_wait(a_full + 8 * d.stage, d.parity, dead);
                     tc_fence_after();
@@ -328,33 +317,35 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             for (int k = k0; ok && k < k1; ++k) {
                 const int count = subs(k);
 #pragma unroll
-                for (int i = 0; i < kSubs; i += C::kSet) {  // a decoded set
+                for (int i = 0; i < kSubs; i += C::kDq) {  // a decoded set
                     if (i >= count) break;
-                    Ring<C::kXStages> xs[C::kSet];          // where its sub-steps' x is
+                    Ring<C::kXStages> xs[C::kDq];          // where its sub-steps' x is
 #pragma unroll
-                    for (int q = 0; q < C::kSet; ++q) {
+                    for (int q = 0; q < C::kDq; ++q) {
                         xs[q] = x;
-                        if ((i + q) % C::kXSubs == 0 && i + q < count)
-                            ok = ok && mbar_wait(x_full + 8 * x.stage, x.parity, dead);
                         if ((i + q) % C::kXSubs == C::kXSubs - 1 && i + q < count) x.next();
                     }
+#pragma unroll
+                    for (int q = 0; q < C::kDq; ++q)
+                        if ((i + q) % C::kXSubs == 0 && i + q < count)
+                            ok = ok && mbar_wait(x_full + 8 * xs[q].stage, xs[q].parity, dead);
                     ok = ok && mbar_wait(a_full + 8 * d.stage, d.parity, dead);
                     if (G > 1) ok = ok && mbar_wait(peer_full + 8 * d.stage, d.parity, dead);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
-                        for (int q = 0; q < C::kSet; ++q) {
+                        for (int q = 0; q < C::kDq; ++q) {
                             if (i + q >= count) break;
                             const uint64_t desc = desc0 + (xs[q].stage * C::kX >> 4) + ((i + q) % C::kXSubs * C::kXTile >> 4);
-                            const uint32_t at = a_tmem + (d.stage * C::kSet + q) * kACols;
+                            const uint32_t at = a_tmem + (d.stage * C::kDq + q) * kACols;
 #pragma unroll
                             for (int c = 0; c < kSubCols / 16; ++c)
                                 tc_mma_bf16<G>(acc, at + c * 8, desc + c * 2, idesc, k > k0 || i + q + c > 0);
                             if ((i + q) % C::kXSubs == C::kXSubs - 1) tc_commit<G>(x_empty + 8 * xs[q].stage);
                         }
                         tc_commit<G>(a_empty + 8 * d.stage);
-                        if (C::kXSubs > 1 && i + C::kSet >= count && count % C::kXSubs != 0)
+                        if (C::kXSubs > 1 && i + C::kDq >= count && count % C::kXSubs != 0)
                             tc_commit<G>(x_empty + 8 * x.stage);
                     }
                     __syncwarp();
@@ -371,11 +362,9 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         }
     } else if (warp >= 4 && warp < 4 + 4 * C::kDq) {
         const int group = (warp - 4) / 4, quarter = warp % 4, row = quarter * 32 + lane;
-        // Each group decodes one piece of every set, or none of the last one of a
-        // ragged step, and waits and signals either way: a group that skipped a
-        // set could take a later phase of its barriers for this one.  (Many
-        // tokens: two groups with 64 columns each took 1150 clocks a set, whose
-        // products take 770.)
+        // Each group decodes one sub-step of every set, or none of the last one
+        // of a ragged step, and waits and signals either way: a group that
+        // skipped a set could take a later phase of its barriers for this one.
         const uint32_t lane_base = smem_u32(table) + 4 * lane;
         if (C::kTable) {                                   // filled while the first copies are on their way
             for (int b = warp - 4; b < 256; b += 4 * C::kDq)
@@ -391,33 +380,22 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 const uint8_t* codes = w_ring + w.stage * C::kWStage + row * 128;
                 const uint8_t* scales = w_ring + w.stage * C::kWStage + C::kW + lane * 16 + quarter * 4;
                 const int n = subs(k);
-                for (int i = 0; i < n; i += C::kSet, d.next()) {
-                    constexpr int kWords = C::kPiece / 8;
-                    const int p = i * (kSubCols / C::kPiece) + group;            // piece of the step
-                    const bool live = p * C::kPiece < n * kSubCols;
-                    uint32_t v[C::kPiece / 2];
-                    if (live) {
-                        uint32_t c[kWords];
-#pragma unroll
-                        for (int q = 0; q < kWords / 4; ++q) {
-                            const uint4 u =
-                                *reinterpret_cast<const uint4*>(codes + ((p * (kWords / 4) + q) ^ (row & 7)) * 16);
-                            c[4 * q] = u.x, c[4 * q + 1] = u.y, c[4 * q + 2] = u.z, c[4 * q + 3] = u.w;
-                        }
-                        // scale bytes of the piece: kPiece / 16 or / 32, of 4 a tile
-                        constexpr int kBytes = C::kPiece / (MX ? 32 : 16), kPer = 4 / kBytes;
-                        const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + p / kPer * 512) >>
-                                            (8 * kBytes * (p % kPer));
+                for (int i = group; i < (n + C::kDq - 1) / C::kDq * C::kDq; i += C::kDq, d.next()) {
+                    uint32_t v[32];
+                    if (i < n) {
+                        const uint4 c0 = *reinterpret_cast<const uint4*>(codes + ((2 * i) ^ (row & 7)) * 16);
+                        const uint4 c1 = *reinterpret_cast<const uint4*>(codes + ((2 * i + 1) ^ (row & 7)) * 16);
+                        const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + (MX ? i / 2 : i) * 512);
+                        const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
                         if (MX)
-                            decode_mxfp4<C::kTable>(c, sc, lane_base, v);
+                            decode_mxfp4<C::kTable>(c, sc >> (16 * (i & 1)), lane_base, v);
                         else
                             decode_nvfp4<C::kTable>(c, sc, lane_base, v);
                     }
                     if (!(ok = mbar_wait(a_empty + 8 * d.stage, d.parity ^ 1, dead))) break;
-                    if (live) {
+                    if (i < n) {
                         tc_fence_after();
-                        tmem_store(a_tmem + d.stage * (C::kSet * kACols) + group * (C::kPiece / 2) +
-                                       ((uint32_t)quarter << 21), v);
+                        tmem_store(a_tmem + (d.stage * C::kDq + group) * kACols + ((uint32_t)quarter << 21), v);
                         tc_fence_before();
                     }
                     __syncwarp();
