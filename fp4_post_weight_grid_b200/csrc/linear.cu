@@ -14,6 +14,8 @@
 //   warp 2     the tile table, then idle;
 //   warps 4..  in kDq groups of four, decode, a sub-step per group at a time;
 //   the last   in groups of four, take the accumulator to y (product_tile.cuh).
+#include <climits>
+
 #include "decode.cuh"
 #include "product_host.cuh"
 
@@ -27,7 +29,14 @@ constexpr int kSubs = kStepCols / kSubCols;
 constexpr int kTableBytes = 65536;
 constexpr int kACols = kSubCols / 2;       // columns of tensor memory per decoded sub-step
 
-template <int BN> struct Config {
+// The tensor core truncates where it adds: after 8192 columns a binary32 result
+// would be off by 3e-6 (a plain binary32 sum by 1.5e-6), after 2048 by 1e-7.  So
+// float results take the accumulator over after every 2048 columns and add the
+// pieces in shared memory.  In bf16 neither shows.
+constexpr int kRun = 2048 / kStepCols;     // steps
+
+template <int BN, typename T> struct Config {
+    static constexpr bool kRuns = sizeof(T) == 4 && BN <= 128;
     static constexpr int kPair = BN > 128 ? 2 : 1;                  // thread blocks of a tile
     static constexpr int kW = 128 * 128, kWStage = kW + 4 * 512;
     static constexpr int kXSubs = BN > 64 ? 1 : 4;                  // sub-steps in a stage of x
@@ -35,7 +44,7 @@ template <int BN> struct Config {
     // Few tokens: codes decoded by table (see decode8_table), which takes the
     // second 64 KB of shared memory; x and the sums lie before it, W behind.
     static constexpr bool kTable = BN <= 32;
-    static constexpr int kWStages = BN > 64 ? 5 : BN > 32 ? 6 : 5;
+    static constexpr int kWStages = BN > 64 ? (kRuns ? 4 : 5) : BN > 32 ? 6 : 5;
     static constexpr int kXStages = BN > 128 ? 6 : BN > 64 ? 4 : BN > 32 ? 2 : BN > 16 ? 2 : 4;
     static constexpr int kAccs = 2;
     static constexpr int kDq = BN <= 64 ? 4 : 2;                    // groups of four decoding warps
@@ -45,7 +54,7 @@ template <int BN> struct Config {
     static constexpr int kUsed = kAccs * BN + kADepth * kDq * kACols;
     static constexpr int kCols = kUsed <= 256 ? 256 : 512;
     static constexpr bool kSplits = BN <= 64;
-    static constexpr int kPart = (kSplits ? BN : 32) * kPartRow * 4;        // sums on their way to y, per group
+    static constexpr int kPart = (kSplits ? BN : kRuns ? BN / kEpi : 32) * kPartRow * 4;     // sums on their way to y, per group
     static constexpr int kSmem = kWStages * kWStage + (kTable ? 2 * kTableBytes : kXStages * kX + kEpi * kPart + 1024);
     static_assert(!kTable || kXStages * kX + kEpi * kPart + 1024 <= kTableBytes - 8192, "room before the table");
     static constexpr int kResident = 1;
@@ -154,11 +163,11 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[32
 }
 
 template <bool MX, int BN, typename T>
-__global__ void __launch_bounds__(Config<BN>::kThreads, Config<BN>::kResident)
+__global__ void __launch_bounds__(Config<BN, T>::kThreads, Config<BN, T>::kResident)
 linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
               const __grid_constant__ TileArgs a)
 {
-    using C = Config<BN>;
+    using C = Config<BN, T>;
     constexpr int G = C::kPair;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[2 * (C::kWStages + C::kXStages + C::kAccs) + 3 * C::kADepth + 3];
@@ -235,6 +244,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     };
     // Tokens of a tile as the tensor core counts them.
     auto mma_cols = [&](const Tile& t) { return (t.rows + 16 * G - 1) / (16 * G) * (16 * G); };
+    const int run = C::kRuns && a.split == 1 ? kRun : INT_MAX;       // steps of an accumulator
     // sub-steps of 64 columns of step k
     auto subs = [&](int k) { return min(kSubs, (a.k - k * kStepCols + kSubCols - 1) / kSubCols); };
 
@@ -311,10 +321,19 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next()) {
             const Tile tl = my_tile(t);
             const uint32_t idesc = idesc_bf16(128 * G, mma_cols(tl));
-            const uint32_t acc = tmem + ac.stage * BN;
+            uint32_t acc = tmem + ac.stage * BN;
             if (!(ok = mbar_wait(acc_empty + 8 * ac.stage, ac.parity ^ 1, dead))) break;
             tc_fence_after();
-            for (int k = k0; ok && k < k1; ++k) {
+            for (int k = k0, first = k0; ok && k < k1; ++k) {
+                if (C::kRuns && k - first == run) {        // the next one, into the other accumulator
+                    if (elect_one()) tc_commit<G>(acc_full + 8 * ac.stage);
+                    __syncwarp();
+                    ac.next();
+                    acc = tmem + ac.stage * BN;
+                    first = k;
+                    if (!(ok = mbar_wait(acc_empty + 8 * ac.stage, ac.parity ^ 1, dead))) break;
+                    tc_fence_after();
+                }
                 const int count = subs(k);
 #pragma unroll
                 for (int i = 0; i < kSubs; i += C::kDq) {  // a decoded set
@@ -341,7 +360,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                             const uint32_t at = a_tmem + (d.stage * C::kDq + q) * kACols;
 #pragma unroll
                             for (int c = 0; c < kSubCols / 16; ++c)
-                                tc_mma_bf16<G>(acc, at + c * 8, desc + c * 2, idesc, k > k0 || i + q + c > 0);
+                                tc_mma_bf16<G>(acc, at + c * 8, desc + c * 2, idesc, k > first || i + q + c > 0);
                             if ((i + q) % C::kXSubs == C::kXSubs - 1) tc_commit<G>(x_empty + 8 * xs[q].stage);
                         }
                         tc_commit<G>(a_empty + 8 * d.stage);
@@ -413,8 +432,30 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         bool ok = true;
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next(), parity ^= 1) {
             const Tile tl = my_tile(t);
-            const uint32_t acc = tmem + ac.stage * BN;
             const float S = MX ? 4.f : a.w_S[tl.group] * 128.f;        // the decoded weights are scaled down
+            auto release = [&](uint32_t stage) {           // the accumulator has been read by this group
+                tc_fence_before();
+                tile_bar(e);
+                if (warp % 4 == 0 && lane == 0) {
+                    if (G > 1)
+                        mbar_signal_peer(acc_empty + 8 * stage, rank & ~1u);
+                    else
+                        mbar_arrive(acc_empty + 8 * stage);
+                }
+            };
+            if (k1 - k0 > run) {
+                float* mine = part + e * (C::kPart / 4);
+                for (int k = k0; k < k1; k += run) {
+                    if (k > k0) ac.next();
+                    ok = mbar_wait_long(acc_full + 8 * ac.stage, ac.parity, dead) && ok;
+                    tc_fence_after();
+                    if (ok) add_to_part<C::kEpi>(tmem + ac.stage * BN, tl.rows, mine, e, k > k0);
+                    release(ac.stage);
+                }
+                if (ok) finish_part<T, C::kEpi>(a, tl, S, mine, e);
+                continue;
+            }
+            const uint32_t acc = tmem + ac.stage * BN;
             ok = mbar_wait_long(acc_full + 8 * ac.stage, ac.parity, dead);
             tc_fence_after();
             if (C::kSplits && a.split > 1) {
@@ -422,14 +463,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                                          acc_empty + 8 * ac.stage) && ok;
             } else {
                 if (ok) write_tile<T, Chunk<T, BN>::kTokens, C::kEpi>(a, tl, acc, S, part + e * (C::kPart / 4), e);
-                tc_fence_before();
-                tile_bar(e);
-                if (warp % 4 == 0 && lane == 0) {
-                    if (G > 1)
-                        mbar_signal_peer(acc_empty + 8 * ac.stage, rank & ~1u);
-                    else
-                        mbar_arrive(acc_empty + 8 * ac.stage);
-                }
+                release(ac.stage);
             }
         }
     }
@@ -451,7 +485,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
 template <bool MX, int BN, typename T>
 static cudaError_t launch_one(const Product& p, TileArgs& a, const TileShape& shape, cudaStream_t s)
 {
-    using C = Config<BN>;
+    using C = Config<BN, T>;
     auto kernel = linear_kernel<MX, BN, T>;
     CUtensorMap w_map, x_map;
     cudaError_t e = byte_tile_map(&w_map, p.w, p.n * p.groups, p.k / 2, 128);
@@ -465,10 +499,7 @@ static cudaError_t launch_one(const Product& p, TileArgs& a, const TileShape& sh
 template <bool MX, typename T> static cudaError_t launch_shape(const Product& p, cudaStream_t s)
 {
     TileArgs a = tile_args(p, kStepCols, MX ? 128 : 64);
-    // The tensor core truncates where it adds: after 8192 columns a binary32
-    // result would be off by 3e-6 (a plain binary32 sum by 1.5e-6), after 2048 it
-    // is off by 1e-7.  For bf16 results neither shows.
-    const TileShape shape = tile_shape(p, a.k_steps, 2, p.out_bf16 ? INT32_MAX : 2048 / kStepCols);
+    const TileShape shape = tile_shape(p, a.k_steps, 2, p.out_bf16 ? INT_MAX : kRun);
     if (shape.tokens <= 16) return launch_one<MX, 16, T>(p, a, shape, s);
     if (shape.tokens <= 32) return launch_one<MX, 32, T>(p, a, shape, s);
     if (shape.tokens <= 64) return launch_one<MX, 64, T>(p, a, shape, s);

@@ -20,6 +20,8 @@
 // same products: what bounds the wide tiles is the way from L2.  Two
 // accumulators of 192 columns let the epilogue of one tile run under the
 // products of the next.
+#include <climits>
+
 #include "product_host.cuh"
 
 namespace fp4q {
@@ -346,7 +348,7 @@ static cudaError_t launch_one(const Product& p, TileArgs& a, const TileShape& sh
 template <bool MX, typename T> static cudaError_t launch_shape(const Product& p, cudaStream_t s)
 {
     TileArgs a = tile_args(p, kStepCols, MX ? 128 : 64);
-    const TileShape shape = tile_shape(p, a.k_steps, 2, INT32_MAX);
+    const TileShape shape = tile_shape(p, a.k_steps, 2, INT_MAX);
     if (shape.tokens <= 16) return launch_one<MX, 16, T>(p, a, shape, s);
     if (shape.tokens <= 32) return launch_one<MX, 32, T>(p, a, shape, s);
     if (shape.tokens <= 64) return launch_one<MX, 64, T>(p, a, shape, s);

@@ -75,7 +75,7 @@ TileArgs tile_args(const Product& p, int step_cols, int scale_tile_cols)
     return a;
 }
 
-TileShape tile_shape(const Product& p, int k_steps, int pair, int longest)
+TileShape tile_shape(const Product& p, int k_steps, int pair, int run)
 {
     const int64_t rows = p.offsets ? (p.m + p.groups - 1) / p.groups : p.m;       // of a group, on average
     const int64_t busy = p.offsets ? std::min<int64_t>(p.groups, p.m) : 1;
@@ -87,33 +87,34 @@ TileShape tile_shape(const Product& p, int k_steps, int pair, int longest)
     // Rounds of tiles over the SMs times the length of one, whose fixed part
     // (the weight's tile, decoded or copied) weighs as much as about 160 tokens:
     // 2048 tokens x 14336 x 4096 took 242, 208 and 201 us in tiles of 128, 160 and
-    // 192, FP4 x FP4 on 4096 tokens 152, 136 and 128 us.
-    auto cost = [&](int tokens) {
+    // 192, FP4 x FP4 on 4096 tokens 152, 136 and 128 us.  Blocks that would idle
+    // may share a tile's steps, which costs them the exchange of the partial
+    // sums, about 40 tokens' worth; only while all of them run at once, as the
+    // exchange is not hidden: one in every round took 16 x 4096 x 14336 to 23 us
+    // from 11 us in one.
+    auto cost = [&](int tokens, int split) {
         const int64_t slots = tokens > 128 ? sms / pair : sms;
-        return (tiles(tokens) + slots - 1) / slots * (tokens + 160);
+        return (tiles(tokens) * split + slots - 1) / slots * (tokens + 160) / split + (split > 1 ? 40 : 0);
     };
+    // Sums longer than a run are put together in shared memory: by one block
+    // alone, and in tiles that fit there.
+    const int most = k_steps > run ? 128 : 192;
     TileShape t{16, 1};
-    while (t.tokens < 128 && t.tokens < rows) t.tokens *= 2;
-    if (rows > 128) {
-        int64_t best = cost(128);
-        for (int tokens = 160; tokens <= 192; tokens += 32)
-            if (p.offsets || cost(tokens) <= best) {       // groups differ: no use in counting rounds
-                best = cost(tokens);
+    int64_t best = INT64_MAX;
+    for (const int tokens : {16, 32, 64, 128, 160, 192}) {
+        if (tokens > most || (tokens >= 32 && tokens / 2 >= rows)) break;
+        for (int split = 1; split <= 8; split *= 2) {
+            if (split > 1 && (tokens > 64 || split > k_steps || tiles(tokens) * split > sms)) break;
+            if (split > 1 && k_steps > run && (k_steps + split - 1) / split > run) continue;
+            if (cost(tokens, split) <= best) {
+                best = cost(tokens, split);
                 t.tokens = tokens;
+                t.split = split;
             }
+        }
     }
-    // Fewer tokens a tile until every SM has one.
-    while (t.tokens > 32 && tiles(t.tokens) < (t.tokens > 128 ? sms / pair : sms))
-        t.tokens = t.tokens > 128 ? 128 : t.tokens / 2;
-    const bool too_long = k_steps > longest;
-    if (too_long) t.tokens = std::min(t.tokens, 64);
-    if (t.tokens <= 64)
-        // Blocks that would idle share the tiles' steps.  Only while all of
-        // them run at once: the exchange of the partial sums is not hidden, and
-        // one in every round cost 16 x 4096 x 14336 23 us, against 11 us in one.
-        while (t.split < 8 && t.split * 2 <= k_steps &&
-               (tiles(t.tokens) * t.split * 2 <= sms || (too_long && t.split * longest < k_steps)))
-            t.split *= 2;
+    // Groups differ: no use in counting rounds of the average one.
+    if (p.offsets && rows > 128 && t.tokens > 64) t.tokens = most;
     return t;
 }
 

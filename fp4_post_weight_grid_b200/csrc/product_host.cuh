@@ -27,9 +27,9 @@ struct TileShape {
     int tokens;      // rows of x per tile, a multiple of 16 (of 32 above 128), at most 192
     int split;       // thread blocks that share a tile's K
 };
-// pair: thread blocks that share a tile of more than 128 tokens; longest: most
-// steps that one accumulator may sum.
-TileShape tile_shape(const Product& p, int k_steps, int pair, int longest);
+// pair: thread blocks that share a tile of more than 128 tokens; run: steps that
+// one accumulator may sum.
+TileShape tile_shape(const Product& p, int k_steps, int pair, int run);
 
 // One launch over all tiles: as many clusters of thread blocks (`pair` or the
 // shape's split) as are resident at once, or as there are tiles, if fewer, each

@@ -234,7 +234,60 @@ __device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uin
     }
 }
 
-// The same where a cluster split the steps: every thread block sends its
+// A tile whose sums come in pieces: group e keeps every kGroups-th 16 tokens in
+// its own `part`, one after the other.
+template <int kGroups> __device__ __forceinline__ void add_to_part(uint32_t acc, int rows, float* part, int e, bool add)
+{
+    const int quarter = (threadIdx.x / 32) % 4, line = quarter * 32 + (threadIdx.x & 31);
+#pragma unroll 1
+    for (int c0 = 16 * e; c0 < rows; c0 += 16 * kGroups, part += 16 * kPartRow) {
+        uint32_t r[16];
+        tmem_load16(r, acc + ((uint32_t)quarter << 21) + c0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float* p = part + i * kPartRow + line;
+            *p = add ? *p + __uint_as_float(r[i]) : __uint_as_float(r[i]);
+        }
+    }
+}
+template <typename T, int kGroups>
+__device__ __forceinline__ void finish_part(const TileArgs& a, const Tile& t, float S, const float* part, int e)
+{
+    constexpr int N = Lanes<T>::kCount, kPer = 128 / N;
+    const int tid = threadIdx.x & 127;
+    if (whole_rows<T>(a)) {
+        const int lane = tid % kPer * N;                   // a thread keeps its features
+        if (t.feature + lane < a.n) {
+            float bias[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) bias[i] = bias_of<T>(a, t, lane + i);
+#pragma unroll 1
+            for (int l = tid / kPer;; l += 128 / kPer) {
+                const int c = l / 16 * (16 * kGroups) + 16 * e + l % 16;
+                if (l / 16 * (16 * kGroups) + 16 * e >= t.rows) break;
+                if (c >= t.rows) continue;
+                const int64_t at = (int64_t)(t.row + c) * a.n + t.feature + lane;
+                const Extra x = load_extra<T>(a.ep, at);
+                float z[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) z[i] = part[l * kPartRow + lane + i] * S + bias[i];
+                activate(z, a.ep.act);
+                finish<T>(a.ep, z, x, at);
+            }
+        }
+    } else if (t.feature + tid < a.n) {
+        const float b = bias_of<T>(a, t, tid);
+        for (int c0 = 16 * e, l = 0; c0 < t.rows; c0 += 16 * kGroups, l += 16)
+            for (int i = 0; i < 16 && c0 + i < t.rows; ++i) {
+                float z[1] = {part[(l + i) * kPartRow + tid] * S + b};
+                activate(z, a.ep.act);
+                finish_one<T>(a.ep, z[0], (int64_t)(t.row + c0 + i) * a.n + t.feature + tid);
+            }
+    }
+    tile_bar(e);
+}
+
+// A tile whose steps a cluster split: every thread block sends its
 // partial sums of token c to block c % split, which adds them in rank order (the
 // result does not depend on timing) and finishes the token.  `full` counts the
 // bytes that arrive here, `empty` has an arrival from every block that sends

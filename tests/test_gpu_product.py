@@ -260,6 +260,30 @@ def test_random(form, fmt, m, n, k):
 
 
 @pytest.mark.parametrize("form,fmt", FORMS, ids=form_ids)
+@pytest.mark.parametrize("m,n,k,counts", [
+    (70, 5000, 4128, None), (150, 5001, 6176, None), (20, 19073, 4128, None), (40, 19072, 4128, None), (3, 700, 16384, None),
+    (33, 8200, 9216, None), (0, 3001, 4640, [200, 0, 90, 17]), (0, 3000, 4640, [1, 140])])
+def test_float_results_of_long_sums(form, fmt, m, n, k, counts):
+    # Exact, and on real values within what pieces of 2048 columns allow.  A piece is 128 additions of 16 columns,
+    # each truncated: off by less than one step, 2U relative to the running sum.  Over many outputs of independent
+    # terms the running sum's norm is at most the result's, so the norm of the error is below 128 * 2U = 1.5e-5 of
+    # it for every piece, and the pieces' errors add as their own parts of the result do.
+    p = Problem(form, fmt, m, n, k, counts=counts, behind=1 if counts else 0, exact=True, bias=True, mul=True)
+    p.w_codes &= 0x99
+    if form == "matmul":
+        p.x &= 0x99
+    p.check(exact=True)
+    p = Problem(form, fmt, m, n, k, counts=counts, behind=1 if counts else 0)
+    y, st = p.run()
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    ref, _ = p.reference()
+    inside = ~torch.isnan(ref)
+    off = (y.double() - ref)[inside]
+    assert float(off.norm() / ref[inside].norm()) <= 128 * 2 * U
+
+
+@pytest.mark.parametrize("form,fmt", FORMS, ids=form_ids)
 def test_output_on_top_of_an_input(form, fmt):
     p = Problem(form, fmt, 70, 136, 288, out=torch.bfloat16, mul=True, residual=True)
     want, _ = p.run()
