@@ -227,8 +227,31 @@ __device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uin
                 finish<T>(a.ep, z, x[k], at + k * step);
             }
         } else if (t.feature + line < a.n) {
-            for (int c = 0; c < rows; ++c)
-                finish_one<T>(a.ep, part[c * kPartRow + line], (int64_t)(t.row + c0 + c) * a.n + t.feature + line);
+            // One feature a thread, 16 tokens' mul and residual asked for at once.
+            // (Pieces from each row's first 16-byte boundary on took longer: the
+            // rows' ends, element by element, held up every warp.)
+            int64_t at1 = (int64_t)(t.row + c0) * a.n + t.feature + line;
+            if (!a.ep.mul && !a.ep.residual) {
+#pragma unroll 4
+                for (int c = 0; c < rows; ++c, at1 += a.n)
+                    static_cast<T*>(a.ep.y)[at1] = from_f32<T>(part[c * kPartRow + line]);
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < rows; c += 16, at1 += 16 * a.n) {
+                    T m[16], r[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        m[i] = a.ep.mul && c + i < rows ? static_cast<const T*>(a.ep.mul)[at1 + i * a.n] : from_f32<T>(1.f);
+                        r[i] = a.ep.residual && c + i < rows ? static_cast<const T*>(a.ep.residual)[at1 + i * a.n]
+                                                             : from_f32<T>(-0.f);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)           // times 1 and plus -0 change nothing
+                        if (c + i < rows)
+                            static_cast<T*>(a.ep.y)[at1 + i * a.n] =
+                                from_f32<T>(part[(c + i) * kPartRow + line] * to_f32<T>(m[i]) + to_f32<T>(r[i]));
+                }
+            }
         }
         tile_bar(e);
     }
