@@ -150,6 +150,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 __syncwarp();
             }
         }
+        await_empty(g, empty, dead);
         drain_ring(g, full, dead);
     } else if (warp == 1 && rank % G != 0) {
         // The odd block of a pair tells the even one, which issues for both,
@@ -211,6 +212,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             if (elect_one()) tc_commit<G>(acc_full + 8 * ac.stage);
             __syncwarp();
         }
+        await_empty(ac, acc_empty, dead);
         if (*dead) {
             if (elect_one()) tc_commit<G>(drain);
             mbar_drain(drain, 0);
@@ -302,7 +304,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             tc_fence_after();
             if (C::kSplits && a.split > 1) {
                 ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, parity, rank, dead,
-                                         acc_empty + 8 * ac.stage) && ok;
+                                         acc_empty + 8 * ac.stage, t + tile_step < tiles) && ok;
             } else {
                 if (ok) write_tile<T, Chunk<T, BN>::kTokens, C::kEpi>(a, tl, acc, S, part + e * (C::kPart / 4), e);
                 tc_fence_before();

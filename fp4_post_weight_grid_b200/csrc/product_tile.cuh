@@ -140,6 +140,14 @@ template <int N> __device__ __forceinline__ void drain_ring(Ring<N> r, uint32_t 
     for (int i = 0; i < N; ++i, r.next()) mbar_drain(full + 8 * r.stage, r.parity ^ 1);
 }
 
+// Before a block ends: every signal that a stage is free has arrived, as none
+// may come after it (a pair's, from the other block).
+template <int N> __device__ __forceinline__ void await_empty(Ring<N> r, uint32_t empty, volatile int* dead)
+{
+    for (int i = 0; i < N; ++i, r.next())
+        if (!mbar_wait(empty + 8 * r.stage, r.parity ^ 1, dead)) return;
+}
+
 // From the accumulator (lane = feature, column = token) to y, by four warps
 // that each own a quarter of the lanes, kChunk tokens at a time through
 // shared memory: a thread writes its feature's sums of the chunk there (rows
@@ -314,12 +322,13 @@ __device__ __forceinline__ void finish_part(const TileArgs& a, const Tile& t, fl
 // partial sums of token c to block c % split, which adds them in rank order (the
 // result does not depend on timing) and finishes the token.  `full` counts the
 // bytes that arrive here, `empty` has an arrival from every block that sends
-// here: this tile's have been read.  (Fetching the partials from the peers
+// here: this tile's have been read (`more`: there is a next one, which waits
+// for that; no signal may reach a block that has ended).  (Fetching the partials from the peers
 // instead took two fences and a round trip more, 1.5 us of a small product.)
 template <typename T>
 __device__ __forceinline__ bool write_tile_split(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part,
                                                  uint32_t full, uint32_t empty, uint32_t parity, uint32_t rank,
-                                                 volatile int* dead, uint32_t acc_empty)
+                                                 volatile int* dead, uint32_t acc_empty, bool more)
 {
     constexpr int N = Lanes<T>::kCount, kPer = 128 / N;
     const int tid = threadIdx.x & 127, quarter = (threadIdx.x / 32) % 4, line = quarter * 32 + (threadIdx.x & 31);
@@ -391,7 +400,7 @@ __device__ __forceinline__ bool write_tile_split(const TileArgs& a, const Tile& 
         }
     }
     tile_bar(0);
-    if (tid < a.split) mbar_signal_peer(empty, tid);
+    if (more && tid < a.split) mbar_signal_peer(empty, tid);
     return ok;
 }
 
