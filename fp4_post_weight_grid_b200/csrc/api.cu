@@ -590,9 +590,11 @@ fp4q_status product_call(fp4q::Product p, fp4q_format fmt, const fp4q_epilogue* 
     p.ep = ep ? *ep : fp4q_epilogue{nullptr, nullptr, nullptr, FP4Q_ACT_NONE};
     if (p.ep.act < FP4Q_ACT_NONE || p.ep.act > FP4Q_ACT_SILU || p.groups > FP4Q_PRODUCT_GROUPS_MAX) return FP4Q_ERR_ARG;
     // Rows and columns are 32-bit coordinates of the tensor copies, with room
-    // for a tile past the end.
-    constexpr int64_t kMost = INT32_MAX - 256;
-    if (p.m < 0 || p.n < 0 || p.k <= 0 || p.k % 32 != 0 || p.m > kMost || p.n > kMost || p.k > kMost ||
+    // for a tile past the end; the columns of bf16 x are counted in bytes.  And a
+    // tile's sums have to end well within the time of a bounded wait, 2^32 clocks:
+    // 2^26 columns take less than 2^30 in the widest tile.
+    constexpr int64_t kMost = INT32_MAX - 256, kMostColumns = 1ll << 26;
+    if (p.m < 0 || p.n < 0 || p.k <= 0 || p.k % 32 != 0 || p.m > kMost || p.n > kMost || p.k > kMostColumns ||
         p.n * p.groups > kMost || !shape_ok(p.m, p.k, 1) || !shape_ok(p.n * p.groups, p.k, 1) || !shape_ok(p.m, p.n, 1))
         return FP4Q_ERR_SHAPE;
     if (p.m == 0 || p.n == 0 || p.groups == 0) return FP4Q_OK;

@@ -573,7 +573,7 @@ fp4q_status fp4q_dequant(fp4q_format format, const uint8_t* codes, const uint8_t
  * Arguments (all four):
  *   fmt         FP4Q_NVFP4 or FP4Q_MXFP4.
  *   m, n, k     rows of x and y, rows of W, columns of both.  k is a positive
- *               multiple of 32 (both formats); m and n are arbitrary.
+ *               multiple of 32 (both formats), at most 2^26; m and n are arbitrary.
  *   x           bf16 [m][k], 16-byte aligned; or
  *   x_codes     [m][k/2] bytes, 16-byte aligned, and
  *   x_scales    [m][k/block] bytes, row-major, 4-byte aligned, and
@@ -600,8 +600,8 @@ fp4q_status fp4q_dequant(fp4q_format format, const uint8_t* codes, const uint8_t
  * The results of a call do not depend on other work or on the run: sums are
  * taken in a fixed order.
  * Errors: FP4Q_ERR_DTYPE (fmt, out_dt), FP4Q_ERR_SHAPE (negative sizes, k not
- * a positive multiple of 32, m, groups * n or k above 2^31 - 1 - 256, a tensor
- * that overflows), FP4Q_ERR_ARG (act, too many groups), FP4Q_ERR_NULL,
+ * a positive multiple of 32 or above 2^26, m or groups * n above 2^31 - 1 - 256,
+ * a tensor that overflows), FP4Q_ERR_ARG (act, too many groups), FP4Q_ERR_NULL,
  * FP4Q_ERR_ALIGN, FP4Q_ERR_CUDA.
  */
 #define FP4Q_FLAG_OFFSETS 8             /* group offsets out of order or range */

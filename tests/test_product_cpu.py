@@ -119,3 +119,11 @@ def test_the_binding_refuses(fq):
     assert e.value.status == fq.ERR_SHAPE
     with pytest.raises(TypeError):
         fq.fp4q_matmul(fq.NVFP4, w[:2], None, S, w, ws, S, y, st)
+
+
+@pytest.mark.parametrize("name", ["linear", "linear_group", "matmul", "matmul_group"])
+def test_rows_too_long_for_a_tile_are_refused(fq, q, name):
+    call = _calls(fq, q)[name]
+    for k in (2 ** 26 + 32, 2 ** 29, 2 ** 30, 2 ** 30 + 64):
+        assert call(k=k, m=1, n=1) == fq.ERR_SHAPE, k
+    assert call(k=2 ** 26, m=1, n=1, y=q + 8) == fq.ERR_ALIGN         # the next check is reached
