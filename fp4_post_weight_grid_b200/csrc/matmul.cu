@@ -21,6 +21,7 @@
 // accumulators of 192 columns let the epilogue of one tile run under the
 // products of the next.
 #include <climits>
+#include <type_traits>
 
 #include "product_host.cuh"
 
@@ -223,73 +224,66 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         // neighbouring bytes, at (r % 32) * 16 + (r / 32) * 4 of that tile.  A
         // step's loads are issued when the one before last has been stored, so
         // that they are on their way while the ring is waited for.  One load a
-        // row where rows start on boundaries of a step's bytes (loads of single
-        // words took four times the L1 lookups, 300 clocks a step of 192 rows).
+        // row where rows start on boundaries of a step's bytes, else two; a loop
+        // for each (one for both, shifting by nothing, cost 4096 x 14336 x 4096 10%).
         constexpr int kRows = (BN + 31) / 32;
         const int64_t scols = a.k / (MX ? 32 : 16), total = (int64_t)a.m * scols;
-        const bool wide = scols % (4 * kScaleTiles) == 0 &&
-                          (reinterpret_cast<uintptr_t>(a.x_scales) & (4 * kScaleTiles - 1)) == 0;
-        uint32_t v[kRows][kScaleTiles];
-        auto load = [&](const Tile& tl, int k) {
-            const int64_t c0 = (int64_t)k * kScaleTiles * 4;
+        auto bring = [&](auto whole) {                     // whether rows start on boundaries
+            constexpr bool kWhole = decltype(whole)::value;
+            Bytes<kScaleTiles> v[kRows];
+            auto load = [&](const Tile& tl, int k) {
+                const int64_t c0 = (int64_t)k * kScaleTiles * 4;
 #pragma unroll
-            for (int q = 0; q < kRows; ++q) {
-                const int r = lane + 32 * q;
-                const bool in = r < tl.rows;
-                const int64_t at = (tl.row + r) * scols + c0;
-                if (wide) {
-                    if (MX) {
-                        const uint2 u = in ? __ldg(reinterpret_cast<const uint2*>(a.x_scales + at)) : make_uint2(0, 0);
-                        v[q][0] = u.x;
-                        v[q][1] = u.y;
-                    } else {
-                        const uint4 u =
-                            in ? __ldg(reinterpret_cast<const uint4*>(a.x_scales + at)) : make_uint4(0, 0, 0, 0);
-                        v[q][0] = u.x;
-                        v[q][1] = u.y;
-                        v[q][kScaleTiles - 2] = u.z;
-                        v[q][kScaleTiles - 1] = u.w;
-                    }
-                } else {
-                    load_bytes<kScaleTiles>(a.x_scales, at, total, in ? (int)min(scols - c0, (int64_t)4 * kScaleTiles) : 0,
-                                            v[q]);
+                for (int q = 0; q < kRows; ++q) {
+                    const int r = lane + 32 * q;
+                    const bool in = r < tl.rows;
+                    const int64_t at = (tl.row + r) * scols + c0;
+                    if (kWhole)
+                        v[q].load_whole(a.x_scales + at, in);
+                    else
+                        v[q].load(a.x_scales, at, total, in ? (int)min(scols - c0, (int64_t)4 * kScaleTiles) : 0);
                 }
-            }
-        };
-        Ring<C::kStages> g;
-        bool ok = true;
-        int64_t t = first_tile;
-        int k = k0;
-        Tile tl;
-        auto next = [&] {                                  // the step after (t, k)
-            g.next();
-            if (++k == k1) {
-                k = k0;
-                t += tile_step;
-                if (t < tiles) tl = my_tile(t);
-            }
-        };
-        if (t < tiles) tl = my_tile(t);
-        if (warp == 3 && t < tiles) next();
-        if (t < tiles) load(tl, k);
-        while (t < tiles) {
-            if (!(ok = mbar_wait(empty + 8 * g.stage, g.parity ^ 1, dead))) break;
-            uint8_t* xs = ring + g.stage * C::kStage + C::kW + C::kX + C::kWS;
-#pragma unroll
-            for (int q = 0; q < kRows; ++q) {
-                const int r = lane + 32 * q;
-                if (r >= BN) break;
-#pragma unroll
-                for (int i = 0; i < kScaleTiles; ++i)
-                    *reinterpret_cast<uint32_t*>(xs + (i * C::kTokenTiles + q / 4) * 512 + lane * 16 + q % 4 * 4) = v[q][i];
-            }
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full + 8 * g.stage);
-            next();
-            if (t < tiles) next();
+            };
+            Ring<C::kStages> g;
+            int64_t t = first_tile;
+            int k = k0;
+            Tile tl;
+            auto next = [&] {                              // the step after (t, k)
+                g.next();
+                if (++k == k1) {
+                    k = k0;
+                    t += tile_step;
+                    if (t < tiles) tl = my_tile(t);
+                }
+            };
+            if (t < tiles) tl = my_tile(t);
+            if (warp == 3 && t < tiles) next();
             if (t < tiles) load(tl, k);
-        }
+            while (t < tiles) {
+                if (!mbar_wait(empty + 8 * g.stage, g.parity ^ 1, dead)) break;
+                uint8_t* xs = ring + g.stage * C::kStage + C::kW + C::kX + C::kWS;
+#pragma unroll
+                for (int q = 0; q < kRows; ++q) {
+                    const int r = lane + 32 * q;
+                    if (r >= BN) break;
+                    uint32_t u[kScaleTiles];
+                    v[q].template words<kWhole>(u);
+#pragma unroll
+                    for (int i = 0; i < kScaleTiles; ++i)
+                        *reinterpret_cast<uint32_t*>(xs + (i * C::kTokenTiles + q / 4) * 512 + lane * 16 + q % 4 * 4) = u[i];
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + 8 * g.stage);
+                next();
+                if (t < tiles) next();
+                if (t < tiles) load(tl, k);
+            }
+        };
+        if (scols % (4 * kScaleTiles) == 0 && (reinterpret_cast<uintptr_t>(a.x_scales) & (4 * kScaleTiles - 1)) == 0)
+            bring(std::true_type{});
+        else
+            bring(std::false_type{});
     } else {
         const int e = (warp - 4) / 4;
         if (G == 1 && cluster) cluster_wait();
