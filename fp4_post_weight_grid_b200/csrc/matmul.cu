@@ -21,7 +21,6 @@
 // accumulators of 192 columns let the epilogue of one tile run under the
 // products of the next.
 #include <climits>
-#include <type_traits>
 
 #include "product_host.cuh"
 

@@ -8,6 +8,8 @@
 // tokens in steps of 16: the same kernel serves one token and thousands.
 #pragma once
 
+#include <type_traits>
+
 #include "product_epilogue.cuh"
 #include "tc.cuh"
 
@@ -142,24 +144,24 @@ template <int N> struct Bytes {
     }
     template <bool kWhole> __device__ __forceinline__ void words(uint32_t (&v)[N]) const
     {
-        if (kWhole) {
+        if constexpr (kWhole) {
 #pragma unroll
             for (int i = 0; i < N; ++i) v[i] = w[i];
-            return;
-        }
-        uint32_t u[2 * N];
+        } else {
+            uint32_t u[2 * N];
 #pragma unroll
-        for (int i = 0; i < 2 * N; ++i) u[i] = w[i];
-        if (N == 4)
+            for (int i = 0; i < 2 * N; ++i) u[i] = w[i];
+            if (N == 4)
 #pragma unroll
-            for (int i = 0; i + 2 < 2 * N; ++i) u[i] = back & 8 ? u[i + 2] : u[i];
+                for (int i = 0; i + 2 < 2 * N; ++i) u[i] = back & 8 ? u[i + 2] : u[i];
 #pragma unroll
-        for (int i = 0; i + 1 < 2 * N; ++i) u[i] = back & 4 ? u[i + 1] : u[i];
+            for (int i = 0; i + 1 < 2 * N; ++i) u[i] = back & 4 ? u[i + 1] : u[i];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int left = count - 4 * i;
-            const uint32_t all = __funnelshift_r(u[i], u[i + 1], 8 * (back & 3));
-            v[i] = left >= 4 ? all : left > 0 ? all & ((1u << (8 * left)) - 1) : 0;
+            for (int i = 0; i < N; ++i) {
+                const int left = count - 4 * i;
+                const uint32_t all = __funnelshift_r(u[i], u[i + 1], 8 * (back & 3));
+                v[i] = left >= 4 ? all : left > 0 ? all & ((1u << (8 * left)) - 1) : 0;
+            }
         }
     }
 
@@ -369,98 +371,102 @@ __device__ __forceinline__ void finish_part(const TileArgs& a, const Tile& t, fl
     tile_bar(e);
 }
 
-// A tile whose steps a cluster split: every thread block sends its
-// partial sums of token c to block c % split, which adds them in rank order (the
-// result does not depend on timing) and finishes the token.  `full` counts the
-// bytes that arrive here, `empty` has an arrival from every block that sends
-// here: this tile's have been read (`more`: there is a next one, which waits
-// for that; no signal may reach a block that has ended).  (Fetching the partials from the peers
-// instead took two fences and a round trip more, 1.5 us of a small product.)
-template <typename T>
-__device__ __forceinline__ bool write_tile_split(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part,
-                                                 uint32_t full, uint32_t empty, uint32_t parity, uint32_t rank,
-                                                 volatile int* dead, uint32_t acc_empty, bool more)
+// A tile whose steps a cluster of kSplit blocks shared: every block sends its
+// partial sums of token c to block c % kSplit, which adds them in rank order (the
+// result does not depend on timing) and finishes the token.  A thread sends its
+// feature's sums of 4 (2, for 8 blocks) tokens at a time and finishes that
+// feature of the block's own tokens; `part` is [rank][tokens / 4][128][4].
+// (Sum by sum, and 16 bytes of y a thread, 512 x 1024 x 1024 of fp4q_linear took
+// 13.3 us, 10.4 this way, 16 tokens 6.8 and 6.0; 128 x 4096 x 4096 of MXFP4 in
+// fp4q_matmul 9.6 and 10.7, for the narrow stores.  Fetching the partials from
+// the peers took two fences and a round trip more.)  `full` counts the bytes that
+// arrive here, `empty` has an arrival from every block that sends here: this
+// tile's have been read (`more`: there is a next one, which waits for that; no
+// signal may reach a block that has ended).
+template <typename T, int kSplit>
+__device__ __forceinline__ bool split_tile(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part,
+                                           uint32_t full, uint32_t empty, uint32_t parity, uint32_t rank,
+                                           volatile int* dead, uint32_t acc_empty, bool more)
 {
-    constexpr int N = Lanes<T>::kCount, kPer = 128 / N;
+    constexpr int V = kSplit == 8 ? 2 : 4, kEach = 16 / kSplit;      // tokens at a time, of 16 to each block
+    using Vec = typename std::conditional<V == 4, uint4, uint2>::type;
     const int tid = threadIdx.x & 127, quarter = (threadIdx.x / 32) % 4, line = quarter * 32 + (threadIdx.x & 31);
-    const int shift = __ffs(a.split) - 1;                  // split is a power of two
-    const int slots = (t.rows + a.split - 1) >> shift;     // tokens of a block, at most
-    const int mine = (t.rows - (int)rank + a.split - 1) >> shift;
-    if (tid == 0) mbar_expect(full, mine * a.split * 512);
+    const int slots = (t.rows + 15) / 16 * kEach;          // tokens of a block, with those past the last row
+    const int mine = (t.rows - (int)rank + kSplit - 1) / kSplit;
+    if (tid == 0) mbar_expect(full, slots * kSplit * 512);
     bool ok = mbar_wait(empty, parity ^ 1, dead);          // the tile before has been read everywhere
     if (ok)
 #pragma unroll 1
         for (int c0 = 0; c0 < t.rows; c0 += 16) {
             uint32_t r[16];
             tmem_load16(r, acc + ((uint32_t)quarter << 21) + c0);
+            const uint32_t to = smem_u32(part + ((int)rank * slots + c0 / kSplit) * 128 + line * V);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int c = c0 + i;
-                if (c < t.rows)
-                    send_f32(smem_u32(part + ((int)rank * slots + (c >> shift)) * 128 + line), __uint_as_float(r[i]), full,
-                             c & (a.split - 1));
-            }
+            for (int d = 0; d < kSplit; ++d)
+#pragma unroll
+                for (int j = 0; j < kEach; j += V) {
+                    Vec v;
+                    v.x = r[j * kSplit + d];
+                    v.y = r[(j + 1) * kSplit + d];
+                    if constexpr (V == 4) {
+                        v.z = r[(j + 2) * kSplit + d];
+                        v.w = r[(j + 3) * kSplit + d];
+                    }
+                    send(to + j * 512, v, full, d);
+                }
         }
     tc_fence_before();
     tile_bar(0);
     if (tid == 0) mbar_arrive(acc_empty);
-    const bool whole = whole_rows<T>(a);
-    const int lane = tid % kPer * N;                       // a thread keeps its features
-    const bool in = whole && t.feature + lane < a.n;
-    int slot = tid / kPer;
-    auto at = [&](int s) { return (int64_t)(t.row + (s << shift) + (int)rank) * a.n + t.feature + lane; };
-    Extra x;
-    float bias[N];
-    if (in && slot < mine) {
-        x = load_extra<T>(a.ep, at(slot));
+    const float bias = bias_of<T>(a, t, tid);
+    const bool in = t.feature + tid < a.n;
+    auto at = [&](int s) { return (int64_t)(t.row + s * kSplit + (int)rank) * a.n + t.feature + tid; };
+    T m[V], res[V];
+    auto load = [&](int s0) {                              // times 1 and plus -0 change nothing
 #pragma unroll
-        for (int i = 0; i < N; ++i) bias[i] = bias_of<T>(a, t, lane + i);
-    }
+        for (int i = 0; i < V; ++i) {
+            const bool here = in && s0 + i < mine;
+            m[i] = a.ep.mul && here ? static_cast<const T*>(a.ep.mul)[at(s0 + i)] : from_f32<T>(1.f);
+            res[i] = a.ep.residual && here ? static_cast<const T*>(a.ep.residual)[at(s0 + i)] : from_f32<T>(-0.f);
+        }
+    };
+    load(0);
     ok = mbar_wait(full, parity, dead) && ok;
-    if (whole) {
+    if (ok && in)
 #pragma unroll 1
-        for (; ok && in && slot < mine; slot += 128 / kPer) {
-            float z[N];
+        for (int s = 0; s < mine; s += V) {
+            float z[V] = {};
 #pragma unroll
-            for (int k = 0; k < N; ++k) z[k] = 0.f;
-#pragma unroll 2
-            for (int q = 0; q < a.split; ++q) {
-#pragma unroll
-                for (int k = 0; k < N; k += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(part + (q * slots + slot) * 128 + lane + k);
-                    z[k] += f.x;
-                    z[k + 1] += f.y;
-                    z[k + 2] += f.z;
-                    z[k + 3] += f.w;
+            for (int q = 0; q < kSplit; ++q) {
+                const Vec v = *reinterpret_cast<const Vec*>(part + (q * slots + s) * 128 + tid * V);
+                z[0] += __uint_as_float(v.x);
+                z[1] += __uint_as_float(v.y);
+                if constexpr (V == 4) {
+                    z[2] += __uint_as_float(v.z);
+                    z[3] += __uint_as_float(v.w);
                 }
             }
 #pragma unroll
-            for (int k = 0; k < N; ++k) z[k] = z[k] * S + bias[k];
-            activate(z, a.ep.act);
-            finish<T>(a.ep, z, x, at(slot));
-            if (slot + 128 / kPer < mine) x = load_extra<T>(a.ep, at(slot + 128 / kPer));
-        }
-    } else if (ok && t.feature + tid < a.n) {
-        const float b = bias_of<T>(a, t, tid);
-#pragma unroll 1
-        for (int s = 0; s < mine; s += 4) {
-            float z[4] = {};
-            for (int q = 0; q < a.split; ++q)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (s + i < mine) z[i] += part[(q * slots + s + i) * 128 + tid];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z[i] = z[i] * S + b;
+            for (int i = 0; i < V; ++i) z[i] = z[i] * S + bias;
             activate(z, a.ep.act);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < V; ++i)
                 if (s + i < mine)
-                    finish_one<T>(a.ep, z[i], (int64_t)(t.row + ((s + i) << shift) + (int)rank) * a.n + t.feature + tid);
+                    static_cast<T*>(a.ep.y)[at(s + i)] = from_f32<T>(z[i] * to_f32<T>(m[i]) + to_f32<T>(res[i]));
+            if (s + V < mine) load(s + V);
         }
-    }
     tile_bar(0);
-    if (more && tid < a.split) mbar_signal_peer(empty, tid);
+    if (more && tid < kSplit) mbar_signal_peer(empty, tid);
     return ok;
+}
+template <typename T>
+__device__ __forceinline__ bool write_tile_split(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part,
+                                                 uint32_t full, uint32_t empty, uint32_t parity, uint32_t rank,
+                                                 volatile int* dead, uint32_t acc_empty, bool more)
+{
+    if (a.split == 2) return split_tile<T, 2>(a, t, acc, S, part, full, empty, parity, rank, dead, acc_empty, more);
+    if (a.split == 4) return split_tile<T, 4>(a, t, acc, S, part, full, empty, parity, rank, dead, acc_empty, more);
+    return split_tile<T, 8>(a, t, acc, S, part, full, empty, parity, rank, dead, acc_empty, more);
 }
 
 }  // namespace fp4q

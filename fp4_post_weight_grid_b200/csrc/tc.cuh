@@ -66,15 +66,25 @@ __device__ __forceinline__ void mbar_signal_peer(uint32_t bar, uint32_t rank)
         "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar), "r"(rank)
         : "memory");
 }
-// A float to the same offset in thread block `rank`, counted there as 4 bytes on `bar`.
-__device__ __forceinline__ void send_f32(uint32_t addr, float v, uint32_t bar, uint32_t rank)
+// Four or two words to the same offset in thread block `rank`, counted there as bytes on `bar`.
+__device__ __forceinline__ void send(uint32_t addr, uint4 v, uint32_t bar, uint32_t rank)
 {
     asm volatile(
         "{\n\t.reg .b32 a, b;\n\t"
-        "mapa.shared::cluster.u32 a, %0, %3;\n\t"
-        "mapa.shared::cluster.u32 b, %2, %3;\n\t"
-        "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [a], %1, [b];\n\t}" ::"r"(addr),
-        "r"(__float_as_uint(v)), "r"(bar), "r"(rank)
+        "mapa.shared::cluster.u32 a, %0, %6;\n\t"
+        "mapa.shared::cluster.u32 b, %5, %6;\n\t"
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [a], {%1, %2, %3, %4}, [b];\n\t}" ::"r"(addr),
+        "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar), "r"(rank)
+        : "memory");
+}
+__device__ __forceinline__ void send(uint32_t addr, uint2 v, uint32_t bar, uint32_t rank)
+{
+    asm volatile(
+        "{\n\t.reg .b32 a, b;\n\t"
+        "mapa.shared::cluster.u32 a, %0, %4;\n\t"
+        "mapa.shared::cluster.u32 b, %3, %4;\n\t"
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [a], {%1, %2}, [b];\n\t}" ::"r"(addr),
+        "r"(v.x), "r"(v.y), "r"(bar), "r"(rank)
         : "memory");
 }
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
