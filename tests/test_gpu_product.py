@@ -254,6 +254,19 @@ def test_epilogue_of_groups(form, fmt):
 
 
 @pytest.mark.parametrize("form,fmt", FORMS, ids=form_ids)
+@pytest.mark.parametrize("m,n,k", [(13, 129, 4128), (13, 136, 4128), (33, 1111, 2080), (50, 2000, 1056)])
+def test_epilogue_of_tiles_whose_columns_are_split(form, fmt, m, n, k):
+    # w of 0 and +-1/2, scales up to 4, |x| <= 24, |mul| <= 4: at most 4128 * 2 * 24 * 2 * 4 = 1.6e6, in units of 1/4
+    for counts in (None, [m, 0, 3]):
+        p = Problem(form, fmt, m if counts is None else 0, n, k, counts=counts, behind=2 if counts else 0, bias=True, mul=True,
+                    residual=True, exact=True)
+        p.w_codes &= 0x99
+        p.check(exact=True)
+    for out in (torch.float32, torch.bfloat16):
+        Problem(form, fmt, m, n, k, act=fq.ACT_SILU, out=out, bias=True, mul=True, residual=True).check()
+
+
+@pytest.mark.parametrize("form,fmt", FORMS, ids=form_ids)
 @pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (7, 1000, 14336), (100, 520, 1056), (700, 1111, 4128)])
 def test_random(form, fmt, m, n, k):
     Problem(form, fmt, m, n, k, out=torch.bfloat16, seed=k).check()
