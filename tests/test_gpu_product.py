@@ -296,6 +296,21 @@ def test_float_results_of_long_sums(form, fmt, m, n, k, counts):
     assert float(off.norm() / ref[inside].norm()) <= 128 * 2 * U
 
 
+@pytest.mark.parametrize("fmt", [fq.NVFP4, fq.MXFP4], ids=["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("m,k", [(1, 32), (5, 256), (40, 1024), (33, 1056), (200, 544), (300, 4096)])
+def test_token_scales_at_any_word(fmt, m, k):
+    # the first and the last rows lie at the ends of the buffer that the loads may not leave
+    p = Problem("matmul", fmt, m, 200, k, exact=True)
+    want, _ = p.run()
+    torch.cuda.synchronize()
+    for words in (1, 2, 3):
+        buf = torch.full((p.x_scales.numel() + 4 * words,), 255, dtype=torch.uint8, device=DEV)
+        p.x_scales = buf[4 * words:].view(p.x_scales.shape).copy_(p.x_scales)
+        y, st = p.run()
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0 and torch.equal(y, want), words
+
+
 @pytest.mark.parametrize("form,fmt", FORMS, ids=form_ids)
 def test_output_on_top_of_an_input(form, fmt):
     p = Problem(form, fmt, 70, 136, 288, out=torch.bfloat16, mul=True, residual=True)
