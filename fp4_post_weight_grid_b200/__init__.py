@@ -954,4 +954,6 @@ def check_status(status: torch.Tensor) -> int:
         raise Fp4qError(ERR_RANGE, "device status")
     if v & FLAG_OFFSETS:
         raise Fp4qError(ERR_ARG, "device status: group offsets out of order or range")
+    if v & FLAG_TIMEOUT:
+        raise Fp4qError(ERR_CUDA, "device status: a wait inside a kernel gave up, its outputs are unspecified")
     return v

@@ -91,7 +91,7 @@ typedef enum { FP4Q_NVFP4 = 0, FP4Q_MXFP4 = 1 } fp4q_format;
 /* Bits OR-ed into *d_status by the device. */
 #define FP4Q_FLAG_NONFINITE 1  /* a NaN or Inf reached the scale search     */
 #define FP4Q_FLAG_RANGE     2  /* NVFP4: max|x| nonzero and outside [2^-64, 2^64] */
-#define FP4Q_FLAG_TIMEOUT   4  /* batch: a tile gave up waiting for its weight's max */
+#define FP4Q_FLAG_TIMEOUT   4  /* a wait inside a kernel gave up: outputs are unspecified */
 
 #define FP4Q_NVFP4_BLOCK 16
 #define FP4Q_MXFP4_BLOCK 32

@@ -127,3 +127,13 @@ def test_rows_too_long_for_a_tile_are_refused(fq, q, name):
     for k in (2 ** 26 + 32, 2 ** 29, 2 ** 30, 2 ** 30 + 64):
         assert call(k=k, m=1, n=1) == fq.ERR_SHAPE, k
     assert call(k=2 ** 26, m=1, n=1, y=q + 8) == fq.ERR_ALIGN         # the next check is reached
+
+
+def test_check_status_raises_every_flag(fq):
+    wants = {fq.FLAG_NONFINITE: fq.ERR_NONFINITE, fq.FLAG_RANGE: fq.ERR_RANGE, fq.FLAG_OFFSETS: fq.ERR_ARG,
+             fq.FLAG_TIMEOUT: fq.ERR_CUDA}
+    for flag, error in wants.items():
+        with pytest.raises(fq.Fp4qError, match="device status") as e:
+            fq.check_status(torch.tensor([flag], dtype=torch.int32))
+        assert e.value.status == error
+    assert fq.check_status(torch.zeros(1, dtype=torch.int32)) == 0
