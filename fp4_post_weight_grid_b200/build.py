@@ -21,7 +21,7 @@ SOURCES = ["api.cu", "absmax.cu", "nvfp4.cu", "mxfp4.cu", "dequant.cu", "batch.c
            "product.cu", "matmul.cu", "linear.cu", "few.cu"]
 HEADERS = ["device.cuh", "launch.h", "screen.cuh", "nvfp4_block.cuh", "mxfp4_block.cuh", "batch.h", "wait.cuh",
            "product.h", "product_epilogue.cuh", "tc.cuh", "product_tile.cuh",
-           "product_host.cuh", "decode.cuh"]
+           "product_host.cuh", "decode.cuh", "mbar_wait.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -374,11 +374,11 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 }
                 if (C::kXSubs > 1 && count % C::kXSubs != 0) x.next();     // a ragged step ends its stage
             }
-            if (elect_one()) tc_commit<G>(acc_full + 8 * ac.stage);
+            if (ok && elect_one()) tc_commit<G>(acc_full + 8 * ac.stage);
             __syncwarp();
         }
         await_empty(ac, acc_empty, dead);
-        if (*dead) {
+        if (__any_sync(~0u, *dead)) {
             if (elect_one()) tc_commit<G>(drain);
             mbar_drain(drain, 0);
         }
@@ -438,7 +438,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             const float S = MX ? 4.f : a.w_S[tl.group] * 128.f;        // the decoded weights are scaled down
             auto release = [&](uint32_t stage) {           // the accumulator has been read by this group
                 tc_fence_before();
-                tile_bar(e);
+                ok = group_all(e, ok);
                 if (warp % 4 == 0 && lane == 0) {
                     if (G > 1)
                         mbar_signal_peer(acc_empty + 8 * stage, rank & ~1u);
@@ -448,9 +448,9 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             };
             if (k1 - k0 > run) {
                 float* mine = part + e * (C::kPart / 4);
-                for (int k = k0; k < k1; k += run) {
+                for (int k = k0; ok && k < k1; k += run) {
                     if (k > k0) ac.next();
-                    ok = mbar_wait_long(acc_full + 8 * ac.stage, ac.parity, dead) && ok;
+                    ok = mbar_wait_long(acc_full + 8 * ac.stage, ac.parity, dead);
                     tc_fence_after();
                     if (ok) add_to_part<C::kEpi>(tmem + ac.stage * BN, tl.rows, mine, e, k > k0);
                     release(ac.stage);
@@ -463,9 +463,9 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             tc_fence_after();
             if (C::kSplits && a.split > 1) {
                 ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, parity, rank, dead,
-                                         acc_empty + 8 * ac.stage, t + tile_step < tiles) && ok;
+                                         acc_empty + 8 * ac.stage, t + tile_step < tiles, ok);
             } else {
-                if (ok) write_tile<T, Chunk<T, BN>::kTokens, C::kEpi>(a, tl, acc, S, part + e * (C::kPart / 4), e);
+                write_tile<T, Chunk<T, BN>::kTokens, C::kEpi>(a, tl, acc, S, part + e * (C::kPart / 4), e, ok);
                 release(ac.stage);
             }
         }
@@ -478,6 +478,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         cluster_arrive();
         cluster_wait();
     }
+    if (*dead) linger();
     tc_fence_after();
     if (warp == 1) tmem_free<G>(tmem, C::kCols);
     if (threadIdx.x == 0 && *dead) atomicOr(a.status, FP4Q_FLAG_TIMEOUT);

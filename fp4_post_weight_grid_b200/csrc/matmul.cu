@@ -209,11 +209,11 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 }
                 __syncwarp();
             }
-            if (elect_one()) tc_commit<G>(acc_full + 8 * ac.stage);
+            if (ok && elect_one()) tc_commit<G>(acc_full + 8 * ac.stage);
             __syncwarp();
         }
         await_empty(ac, acc_empty, dead);
-        if (*dead) {
+        if (__any_sync(~0u, *dead)) {
             if (elect_one()) tc_commit<G>(drain);
             mbar_drain(drain, 0);
         }
@@ -297,11 +297,11 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             tc_fence_after();
             if (C::kSplits && a.split > 1) {
                 ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, parity, rank, dead,
-                                         acc_empty + 8 * ac.stage, t + tile_step < tiles) && ok;
+                                         acc_empty + 8 * ac.stage, t + tile_step < tiles, ok);
             } else {
-                if (ok) write_tile<T, Chunk<T, BN>::kTokens, C::kEpi>(a, tl, acc, S, part + e * (C::kPart / 4), e);
+                write_tile<T, Chunk<T, BN>::kTokens, C::kEpi>(a, tl, acc, S, part + e * (C::kPart / 4), e, ok);
                 tc_fence_before();
-                tile_bar(e);
+                ok = group_all(e, ok);
                 if (warp % 4 == 0 && lane == 0) {
                     if (G > 1)
                         mbar_signal_peer(acc_empty + 8 * ac.stage, rank & ~1u);
@@ -319,6 +319,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         cluster_arrive();
         cluster_wait();
     }
+    if (*dead) linger();
     tc_fence_after();
     if (warp == 1) tmem_free<G>(tmem, C::kCols);
     if (threadIdx.x == 0 && *dead) atomicOr(a.status, FP4Q_FLAG_TIMEOUT);

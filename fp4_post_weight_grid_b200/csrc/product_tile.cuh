@@ -211,9 +211,6 @@ template <typename T, int BN> struct Chunk {
     static constexpr int kTokens = BN < 4 * Lanes<T>::kCount ? BN : 4 * Lanes<T>::kCount;
 };
 
-// The barrier of group `e` of four epilogue warps.
-__device__ __forceinline__ void tile_bar(int e) { asm volatile("bar.sync %0, 128;" ::"r"(1 + e) : "memory"); }
-
 // Columns [c0, c0 + count) of the accumulator; S, bias and act are applied
 // on the way where `last` (the sums are complete).
 template <bool last>
@@ -250,9 +247,11 @@ template <typename T> __device__ __forceinline__ float bias_of(const TileArgs& a
 }
 
 // A tile that needs no sum over a cluster; group e of kGroups takes every
-// kGroups-th chunk, through a `part` of its own.
+// kGroups-th chunk, through a `part` of its own.  `ok`, the warp's: the sums are
+// there; the group writes where they are for all of its warps.
 template <typename T, int kChunk, int kGroups>
-__device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part, int e)
+__device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part, int e,
+                                           bool ok)
 {
     constexpr int N = Lanes<T>::kCount, kPer = 128 / N, kItems = kChunk * kPer / 128;
     const int tid = threadIdx.x & 127, line = (threadIdx.x / 32) % 4 * 32 + (threadIdx.x & 31);
@@ -269,8 +268,9 @@ __device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uin
 #pragma unroll
         for (int k = 0; k < kItems; ++k)
             if (in && token0 + k * (128 / kPer) < rows) x[k] = load_extra<T>(a.ep, at + k * step);
-        to_part<true>(acc, c0, rows, part, S, bias, a.ep.act);
-        tile_bar(e);
+        if (ok) to_part<true>(acc, c0, rows, part, S, bias, a.ep.act);
+        ok = group_all(e, ok);
+        if (!ok) return;
         if (whole) {
 #pragma unroll
             for (int k = 0; k < kItems; ++k) {
@@ -314,7 +314,7 @@ __device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uin
                 }
             }
         }
-        tile_bar(e);
+        group_bar(e);
     }
 }
 
@@ -368,7 +368,7 @@ __device__ __forceinline__ void finish_part(const TileArgs& a, const Tile& t, fl
                 finish_one<T>(a.ep, z[0], (int64_t)(t.row + c0 + i) * a.n + t.feature + tid);
             }
     }
-    tile_bar(e);
+    group_bar(e);
 }
 
 // A tile whose steps a cluster of kSplit blocks shared: every block sends its
@@ -383,10 +383,12 @@ __device__ __forceinline__ void finish_part(const TileArgs& a, const Tile& t, fl
 // arrive here, `empty` has an arrival from every block that sends here: this
 // tile's have been read (`more`: there is a next one, which waits for that; no
 // signal may reach a block that has ended).
+// `ok`, the warp's: its sums are there.  Returns, to all of the group, whether no
+// wait gave up.
 template <typename T, int kSplit>
 __device__ __forceinline__ bool split_tile(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part,
                                            uint32_t full, uint32_t empty, uint32_t parity, uint32_t rank,
-                                           volatile int* dead, uint32_t acc_empty, bool more)
+                                           volatile int* dead, uint32_t acc_empty, bool more, bool ok)
 {
     constexpr int V = kSplit == 8 ? 2 : 4, kEach = 16 / kSplit;      // tokens at a time, of 16 to each block
     using Vec = typename std::conditional<V == 4, uint4, uint2>::type;
@@ -394,7 +396,7 @@ __device__ __forceinline__ bool split_tile(const TileArgs& a, const Tile& t, uin
     const int slots = (t.rows + 15) / 16 * kEach;          // tokens of a block, with those past the last row
     const int mine = (t.rows - (int)rank + kSplit - 1) / kSplit;
     if (tid == 0) mbar_expect(full, slots * kSplit * 512);
-    bool ok = mbar_wait(empty, parity ^ 1, dead);          // the tile before has been read everywhere
+    ok = ok && mbar_wait(empty, parity ^ 1, dead);         // the tile before has been read everywhere
     if (ok)
 #pragma unroll 1
         for (int c0 = 0; c0 < t.rows; c0 += 16) {
@@ -416,7 +418,7 @@ __device__ __forceinline__ bool split_tile(const TileArgs& a, const Tile& t, uin
                 }
         }
     tc_fence_before();
-    tile_bar(0);
+    group_bar(0);
     if (tid == 0) mbar_arrive(acc_empty);
     const float bias = bias_of<T>(a, t, tid);
     const bool in = t.feature + tid < a.n;
@@ -431,7 +433,7 @@ __device__ __forceinline__ bool split_tile(const TileArgs& a, const Tile& t, uin
         }
     };
     load(0);
-    ok = mbar_wait(full, parity, dead) && ok;
+    ok = ok && mbar_wait(full, parity, dead);
     if (ok && in)
 #pragma unroll 1
         for (int s = 0; s < mine; s += V) {
@@ -455,18 +457,18 @@ __device__ __forceinline__ bool split_tile(const TileArgs& a, const Tile& t, uin
                     static_cast<T*>(a.ep.y)[at(s + i)] = from_f32<T>(z[i] * to_f32<T>(m[i]) + to_f32<T>(res[i]));
             if (s + V < mine) load(s + V);
         }
-    tile_bar(0);
+    ok = group_all(0, ok);
     if (more && tid < kSplit) mbar_signal_peer(empty, tid);
     return ok;
 }
 template <typename T>
 __device__ __forceinline__ bool write_tile_split(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part,
                                                  uint32_t full, uint32_t empty, uint32_t parity, uint32_t rank,
-                                                 volatile int* dead, uint32_t acc_empty, bool more)
+                                                 volatile int* dead, uint32_t acc_empty, bool more, bool ok)
 {
-    if (a.split == 2) return split_tile<T, 2>(a, t, acc, S, part, full, empty, parity, rank, dead, acc_empty, more);
-    if (a.split == 4) return split_tile<T, 4>(a, t, acc, S, part, full, empty, parity, rank, dead, acc_empty, more);
-    return split_tile<T, 8>(a, t, acc, S, part, full, empty, parity, rank, dead, acc_empty, more);
+    if (a.split == 2) return split_tile<T, 2>(a, t, acc, S, part, full, empty, parity, rank, dead, acc_empty, more, ok);
+    if (a.split == 4) return split_tile<T, 4>(a, t, acc, S, part, full, empty, parity, rank, dead, acc_empty, more, ok);
+    return split_tile<T, 8>(a, t, acc, S, part, full, empty, parity, rank, dead, acc_empty, more, ok);
 }
 
 }  // namespace fp4q

@@ -1,9 +1,5 @@
 // tc.cuh -- sm_100a tensor-core, tensor-copy and barrier primitives used by
 // the products on FP4 weights.
-//
-// Every wait is bounded by time: a wait that runs out sets the thread block's
-// `dead` word, every other wait of the block then ends at its next look at it,
-// and the kernel reports FP4Q_FLAG_TIMEOUT.
 #pragma once
 
 #include <cstdint>
@@ -97,48 +93,25 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
-constexpr long long kWaitClocks = 1ll << 32;    // longest wait: about two seconds of SM clocks
+// The barrier of group `e` of four epilogue warps; group_all also gives all of
+// them whether `ok` held for every thread.
+__device__ __forceinline__ void group_bar(int e) { asm volatile("bar.sync %0, 128;" ::"r"(1 + e) : "memory"); }
+__device__ __forceinline__ bool group_all(int e, bool ok)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+        "bar.red.and.pred q, %1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"(1 + e), "r"((uint32_t)ok) : "memory");
+    return r != 0;
+}
 
-// True once the barrier's phase `parity` has completed; false if the thread
-// block is dead or the wait ran out (which makes it dead).  Time is the SM's
-// own clock.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead)
-{
-    if (mbar_try(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try(bar, parity)) return true;
-        if (*dead) return false;
-        if (clock64() - t0 > kWaitClocks) {
-            *dead = 1;
-            return false;
-        }
-    }
-}
-// For a long wait (the epilogue's for a tile's sums): looks seldom, so that the
-// waiting warps leave the issue slots to the ones that work.
-__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* dead)
-{
-    const long long t0 = clock64();
-    while (!mbar_try(bar, parity)) {
-        __nanosleep(64);
-        if (*dead) return false;
-        if (clock64() - t0 > kWaitClocks) {
-            *dead = 1;
-            return false;
-        }
-    }
-    return true;
-}
-// For the end of a dead thread block: the wait for what it has in flight.
-__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity)
-{
-    const long long t0 = clock64();
-    while (!mbar_try(bar, parity) && clock64() - t0 < kWaitClocks / 16) {
-    }
-}
+}  // namespace fp4q
+
+#include "mbar_wait.cuh"
+
+namespace fp4q {
 
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_rank()
