@@ -20,6 +20,13 @@
 // 15.7 against 16.6 and 16.8; 4096 x 14336 15.1 and 19.8 against 16.5 and 16.9;
 // 28672 x 8192 47.0 and 50.6 against 47.5.  It is bound by instructions (about
 // 240 a warp for 2048 weights, 150 of them decoding, issue slots two thirds busy).
+//
+// The tensor core truncates where it adds, so a long sum in one accumulator
+// falls short by an amount that grows with its length (by 3e-5 of it after 32768
+// columns): after every 2048 columns of a warp the sums go to registers of their
+// own, by additions that round, and stay within 2e-6 of the whole.  A count of
+// stretches takes 1 x 4096 x 14336 from 14.8 to 15.1 us; at every end of a phase
+// of x it took 15.6.
 #include "decode.cuh"
 #include "product_host.cuh"
 
@@ -31,6 +38,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStretch = 256;                  // columns a warp takes at a time
 constexpr int kTokens = 8;
+constexpr int kRun = 2048;                     // columns that one accumulator may sum
+constexpr int kMostPhase = 4096;               // columns of x in shared memory: 64 KB
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
@@ -149,7 +158,8 @@ few_kernel(const __grid_constant__ TileArgs a, const uint8_t* __restrict__ w, co
         row[h] = w + j * (a.k / 2) + 16 * t;
         scale_row[h] = a.w_scales + j / 128 * a.w_col_tiles * 512 + j % 32 * 16 + j % 128 / 32 * 4;
     }
-    float acc[4] = {};
+    float sum[4] = {}, acc[4] = {};
+    int left = kRun / kStretch;
     Part<MX> next;
     if (part < stretches) next.load(row, scale_row, part, t, a.k - part * kStretch - 32 * t);
     int s = part;
@@ -181,11 +191,21 @@ few_kernel(const __grid_constant__ TileArgs a, const uint8_t* __restrict__ w, co
                 multiply<MX, true>(acc, cur, f, rest, at, g, t);
             else
                 multiply<MX, false>(acc, cur, f, rest, at, g, t);
+            if (--left == 0) {                             // of this run
+                left = kRun / kStretch;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sum[i] += acc[i];
+                    acc[i] = 0.f;
+                }
+            }
         }
     }
-    // acc[0..3]: (row g, tokens 2t and 2t + 1), (row g + 8, the same)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sums[warp][2 * t + i % 2][8 * (i / 2) + g] = acc[i];
+    for (int i = 0; i < 4; ++i) sum[i] += acc[i];
+    // sum[0..3]: (row g, tokens 2t and 2t + 1), (row g + 8, the same)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[warp][2 * t + i % 2][8 * (i / 2) + g] = sum[i];
     __syncthreads();
     const float S = MX ? 4.f : *a.w_S * 128.f;             // the decoded weights are scaled down
     for (int i = threadIdx.x; i < kRows * tiles * a.m; i += kThreads) {
@@ -204,13 +224,12 @@ few_kernel(const __grid_constant__ TileArgs a, const uint8_t* __restrict__ w, co
 template <bool MX, typename T> cudaError_t launch_one(const Product& p, cudaStream_t s)
 {
     const TileArgs a = tile_args(p, kStretch, MX ? 128 : 64);
-    constexpr int kMostPhase = 4096;                       // 64 KB
-    const int phase = (int)std::min<int64_t>((p.k + kStretch - 1) / kStretch * kStretch, kMostPhase);
     // As many warps to a row as leave all blocks resident at once: 4096 rows took
     // 6.3, 7.2, 11.3 and 19.2 us with 8, 4, 2 and 1, 14336 rows 22.5, 18.0, 16.1 and
     // 18.0.
     int ks = 8;
     while (ks > 1 && (p.n * ks + 127) / 128 > 2 * sm_count()) ks /= 2;
+    const int phase = (int)std::min<int64_t>((p.k + kStretch - 1) / kStretch * kStretch, kMostPhase);
     static Residency residency;
     product_blocks_per_sm(residency, reinterpret_cast<const void*>(few_kernel<MX, T>), kThreads,
                           (size_t)kTokens * kMostPhase * 2);

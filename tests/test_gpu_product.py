@@ -296,6 +296,25 @@ def test_float_results_of_long_sums(form, fmt, m, n, k, counts):
     assert float(off.norm() / ref[inside].norm()) <= 128 * 2 * U
 
 
+def _norm_off(p):
+    y, st = p.run()
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    ref, _ = p.reference()
+    return float((y.double() - ref).norm() / ref.norm())
+
+
+@pytest.mark.parametrize("fmt", [fq.NVFP4, fq.MXFP4], ids=NAMES.get)
+@pytest.mark.parametrize("m,n,k", [(1, 64, 65536), (2, 128, 262144), (4, 16, 1 << 20), (3, 19000, 3520), (8, 5000, 8192)])
+def test_float_results_of_few_tokens_on_long_columns(fmt, m, n, k):
+    # A piece of 2048 columns is 128 additions of 16 columns, each truncated: off by at most one step, 2U of the
+    # running sum, and by half a step, U, on average over many outputs.  The running sum's norm after i of them
+    # is sqrt(i / 128) of the piece's, so the norm of the piece's error is below U * 128 * 2/3 of its own.  The
+    # pieces (independent, as their terms are) add up like their errors.  The additions of the pieces round to
+    # nearest: U each, of either sign; at most 256 per warp here, sqrt(256) * U, well below.
+    assert _norm_off(Problem("linear", fmt, m, n, k, seed=k + n)) <= U * 128 * 2 / 3
+
+
 @pytest.mark.parametrize("fmt", [fq.NVFP4, fq.MXFP4], ids=["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("m,k", [(1, 32), (5, 256), (40, 1024), (33, 1056), (200, 544), (300, 4096)])
 def test_token_scales_at_any_word(fmt, m, k):
