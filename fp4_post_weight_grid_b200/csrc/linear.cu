@@ -29,14 +29,15 @@ constexpr int kSubs = kStepCols / kSubCols;
 constexpr int kTableBytes = 65536;
 constexpr int kACols = kSubCols / 2;       // columns of tensor memory per decoded sub-step
 
-// The tensor core truncates where it adds: after 8192 columns a binary32 result
-// would be off by 3e-6 (a plain binary32 sum by 1.5e-6), after 2048 by 1e-7.  So
-// float results take the accumulator over after every 2048 columns and add the
-// pieces in shared memory.  In bf16 neither shows.
-constexpr int kRun = 2048 / kStepCols;     // steps
+// The tensor core truncates where it adds: a float result falls short by 1.2e-6
+// of its norm after 2048 columns, by 3.3e-6 after 8192, 2.6e-5 after 65536 (a
+// plain binary32 sum of 8192 is off by 8e-7).  So longer float sums come in runs
+// of 2048 columns that are added in shared memory (RUNS); bf16 ones, whose
+// rounding is 2e-3, in runs of 65536.
+template <typename T> constexpr int kRun = (sizeof(T) == 4 ? 2048 : 65536) / kStepCols;      // steps
 
-template <int BN, typename T> struct Config {
-    static constexpr bool kRuns = sizeof(T) == 4 && BN <= 128;
+template <int BN, typename T, bool RUNS> struct Config {
+    static constexpr bool kRuns = RUNS;
     static constexpr int kPair = BN > 128 ? 2 : 1;                  // thread blocks of a tile
     static constexpr int kW = 128 * 128, kWStage = kW + 4 * 512;
     static constexpr int kXSubs = BN > 64 ? 1 : 4;                  // sub-steps in a stage of x
@@ -162,12 +163,12 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[32
         : "memory");
 }
 
-template <bool MX, int BN, typename T>
-__global__ void __launch_bounds__(Config<BN, T>::kThreads, Config<BN, T>::kResident)
+template <bool MX, int BN, typename T, bool RUNS>
+__global__ void __launch_bounds__(Config<BN, T, RUNS>::kThreads, Config<BN, T, RUNS>::kResident)
 linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
               const __grid_constant__ TileArgs a)
 {
-    using C = Config<BN, T>;
+    using C = Config<BN, T, RUNS>;
     constexpr int G = C::kPair;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[2 * (C::kWStages + C::kXStages + C::kAccs) + 3 * C::kADepth + 3];
@@ -244,7 +245,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
     };
     // Tokens of a tile as the tensor core counts them.
     auto mma_cols = [&](const Tile& t) { return (t.rows + 16 * G - 1) / (16 * G) * (16 * G); };
-    const int run = C::kRuns && a.split == 1 ? kRun : INT_MAX;       // steps of an accumulator
+    const int run = C::kRuns && a.split == 1 ? kRun<T> : INT_MAX;       // steps of an accumulator
     // sub-steps of 64 columns of step k
     auto subs = [&](int k) { return min(kSubs, (a.k - k * kStepCols + kSubCols - 1) / kSubCols); };
 
@@ -486,11 +487,11 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
 
 }  // namespace
 
-template <bool MX, int BN, typename T>
+template <bool MX, int BN, typename T, bool RUNS = sizeof(T) == 4 && BN <= 128>
 static cudaError_t launch_one(const Product& p, TileArgs& a, const TileShape& shape, cudaStream_t s)
 {
-    using C = Config<BN, T>;
-    auto kernel = linear_kernel<MX, BN, T>;
+    using C = Config<BN, T, RUNS>;
+    auto kernel = linear_kernel<MX, BN, T, RUNS>;
     CUtensorMap w_map, x_map;
     cudaError_t e = byte_tile_map(&w_map, p.w, p.n * p.groups, p.k / 2, 128);
     if (e == cudaSuccess) e = byte_tile_map(&x_map, p.x, p.m, p.k * 2, shape.tokens / C::kPair);
@@ -503,7 +504,8 @@ static cudaError_t launch_one(const Product& p, TileArgs& a, const TileShape& sh
 template <bool MX, typename T> static cudaError_t launch_shape(const Product& p, cudaStream_t s)
 {
     TileArgs a = tile_args(p, kStepCols, MX ? 128 : 64);
-    const TileShape shape = tile_shape(p, a.k_steps, 2, p.out_bf16 ? INT_MAX : kRun);
+    const TileShape shape = tile_shape(p, a.k_steps, 2, kRun<T>, p.out_bf16 ? 64 : 128);
+    if (p.out_bf16 && a.k_steps > kRun<T> && shape.split == 1) return launch_one<MX, 64, T, true>(p, a, shape, s);
     if (shape.tokens <= 16) return launch_one<MX, 16, T>(p, a, shape, s);
     if (shape.tokens <= 32) return launch_one<MX, 32, T>(p, a, shape, s);
     if (shape.tokens <= 64) return launch_one<MX, 64, T>(p, a, shape, s);

@@ -20,8 +20,6 @@
 // same products: what bounds the wide tiles is the way from L2.  Two
 // accumulators of 192 columns let the epilogue of one tile run under the
 // products of the next.
-#include <climits>
-
 #include "product_host.cuh"
 
 namespace fp4q {
@@ -31,13 +29,22 @@ namespace {
 constexpr int kStepCols = 256;             // columns of a step: 128 bytes of codes
 constexpr int kMmaCols = 64;
 
-template <int BN> struct Config {
+// The tensor core truncates where it adds: a float result falls short by 4e-7 of
+// its norm after 2048 columns, 9e-7 after 4096, 1.9e-5 after 65536 (a plain
+// binary32 sum of 4096 is off by 4e-7).  So longer float sums come in runs of
+// 4096 columns that are added in shared memory (RUNS), which leaves room for
+// fewer stages: 4096 x 4096 x 14336 NVFP4 takes 143 us so, 128 with the one
+// accumulator, 140 with the sums in the epilogue's registers.  bf16 ones, whose
+// rounding is 2e-3, come in runs of 65536.
+template <typename T> constexpr int kRun = (sizeof(T) == 4 ? 4096 : 65536) / kStepCols;      // steps
+
+template <int BN, bool RUNS> struct Config {
     static constexpr int kPair = BN > 128 ? 2 : 1;                  // thread blocks of a tile
     static constexpr int kTokenTiles = (BN + 127) / 128;            // scale tiles over the tokens
     static constexpr int kW = 128 * 128, kX = BN / kPair * 128;     // bytes of a step
     static constexpr int kWS = 4 * 512, kXS = kTokenTiles * 4 * 512;
     static constexpr int kStage = kW + kX + kWS + kXS;
-    static constexpr int kStages = BN > 32 ? 5 : 8;
+    static constexpr int kStages = BN > 128 && RUNS ? 3 : BN > 64 && RUNS ? 4 : BN > 32 ? 5 : 8;
     static constexpr int kAccs = 2;
     // Tensor memory: accumulators, then the scales of the last two steps.
     static constexpr int kScaleCols = 4 * 4 * (1 + kTokenTiles);
@@ -45,7 +52,7 @@ template <int BN> struct Config {
     static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     static constexpr bool kSplits = BN <= 64;
     static constexpr int kEpi = BN >= 128 ? 2 : 1;                  // groups of four epilogue warps
-    static constexpr int kPart = (kSplits ? BN : 32) * kPartRow * 4;        // sums on their way to y, per group
+    static constexpr int kPart = (kSplits ? BN : RUNS ? BN / kEpi : 32) * kPartRow * 4;      // sums on their way to y, per group
     static constexpr int kThreads = (4 + 4 * kEpi) * 32;
     static constexpr int kSmem = kStages * kStage + kEpi * kPart + 1024;
     static constexpr int kResident = 1;
@@ -53,12 +60,12 @@ template <int BN> struct Config {
     static_assert(kSmem <= 222 * 1024 && kStage % 1024 == 0, "shared memory");
 };
 
-template <bool MX, int BN, typename T>
-__global__ void __launch_bounds__(Config<BN>::kThreads, Config<BN>::kResident)
+template <bool MX, int BN, typename T, bool RUNS>
+__global__ void __launch_bounds__(Config<BN, RUNS>::kThreads, Config<BN, RUNS>::kResident)
 matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
               const __grid_constant__ TileArgs a)
 {
-    using C = Config<BN>;
+    using C = Config<BN, RUNS>;
     constexpr int G = C::kPair;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[3 * C::kStages + 2 * C::kAccs + 3];
@@ -171,9 +178,17 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next()) {
             const Tile tl = my_tile(t);
             const uint32_t cols = mma_cols(tl);
-            const uint32_t acc = tmem + ac.stage * BN;
+            uint32_t acc = tmem + ac.stage * BN;
             if (!(ok = mbar_wait(acc_empty + 8 * ac.stage, ac.parity ^ 1, dead))) break;
-            for (int k = k0; k < k1; ++k, g.next(), ++step) {
+            for (int k = k0, first = k0; k < k1; ++k, g.next(), ++step) {
+                if (RUNS && k - first == kRun<T>) {        // the next run, into the other accumulator
+                    if (elect_one()) tc_commit<G>(acc_full + 8 * ac.stage);
+                    __syncwarp();
+                    ac.next();
+                    acc = tmem + ac.stage * BN;
+                    first = k;
+                    if (!(ok = mbar_wait(acc_empty + 8 * ac.stage, ac.parity ^ 1, dead))) break;
+                }
                 ok = mbar_wait(full + 8 * g.stage, g.parity, dead);
                 if (G > 1) ok = ok && mbar_wait(peer_full + 8 * g.stage, g.parity, dead);
                 if (step >= 2) {                           // whose scales were where this step's go
@@ -203,7 +218,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                         const int st = MX ? i / 2 : i;
                         tc_mma_fp4<MX, G>(acc, wd + i * 2, xd + i * 2,
                                           idesc_fp4(MX, 128 * G, cols, MX ? (i % 2) * 2 : 0), sf + st * 4,
-                                          sf + 16 + st * 4 * C::kTokenTiles, k > k0 || i > 0);
+                                          sf + 16 + st * 4 * C::kTokenTiles, k > first || i > 0);
                     }
                     tc_commit<G>(empty + 8 * g.stage);
                 }
@@ -291,8 +306,30 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         bool ok = true;
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next(), parity ^= 1) {
             const Tile tl = my_tile(t);
-            const uint32_t acc = tmem + ac.stage * BN;
             const float S = MX ? 1.f : a.w_S[tl.group] * *a.x_S;
+            auto release = [&](uint32_t stage) {           // the accumulator has been read by this group
+                tc_fence_before();
+                ok = group_all(e, ok);
+                if (warp % 4 == 0 && lane == 0) {
+                    if (G > 1)
+                        mbar_signal_peer(acc_empty + 8 * stage, rank & ~1u);
+                    else
+                        mbar_arrive(acc_empty + 8 * stage);
+                }
+            };
+            if (RUNS) {
+                float* mine = part + e * (C::kPart / 4);
+                for (int k = k0; ok && k < k1; k += kRun<T>) {
+                    if (k > k0) ac.next();
+                    ok = mbar_wait_long(acc_full + 8 * ac.stage, ac.parity, dead);
+                    tc_fence_after();
+                    if (ok) add_to_part<C::kEpi>(tmem + ac.stage * BN, tl.rows, mine, e, k > k0);
+                    release(ac.stage);
+                }
+                if (ok) finish_part<T, C::kEpi>(a, tl, S, mine, e);
+                continue;
+            }
+            const uint32_t acc = tmem + ac.stage * BN;
             ok = mbar_wait_long(acc_full + 8 * ac.stage, ac.parity, dead);
             tc_fence_after();
             if (C::kSplits && a.split > 1) {
@@ -300,14 +337,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                                          acc_empty + 8 * ac.stage, t + tile_step < tiles, ok);
             } else {
                 write_tile<T, Chunk<T, BN>::kTokens, C::kEpi>(a, tl, acc, S, part + e * (C::kPart / 4), e, ok);
-                tc_fence_before();
-                ok = group_all(e, ok);
-                if (warp % 4 == 0 && lane == 0) {
-                    if (G > 1)
-                        mbar_signal_peer(acc_empty + 8 * ac.stage, rank & ~1u);
-                    else
-                        mbar_arrive(acc_empty + 8 * ac.stage);
-                }
+                release(ac.stage);
             }
         }
     }
@@ -327,11 +357,11 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
 
 }  // namespace
 
-template <bool MX, int BN, typename T>
+template <bool MX, int BN, typename T, bool RUNS = false>
 static cudaError_t launch_one(const Product& p, TileArgs& a, const TileShape& shape, cudaStream_t s)
 {
-    using C = Config<BN>;
-    auto kernel = matmul_kernel<MX, BN, T>;
+    using C = Config<BN, RUNS>;
+    auto kernel = matmul_kernel<MX, BN, T, RUNS>;
     CUtensorMap w_map, x_map;
     cudaError_t e = byte_tile_map(&w_map, p.w, p.n * p.groups, p.k / 2, 128);
     if (e == cudaSuccess) e = byte_tile_map(&x_map, p.x, p.m, p.k / 2, shape.tokens / C::kPair);
@@ -344,7 +374,14 @@ static cudaError_t launch_one(const Product& p, TileArgs& a, const TileShape& sh
 template <bool MX, typename T> static cudaError_t launch_shape(const Product& p, cudaStream_t s)
 {
     TileArgs a = tile_args(p, kStepCols, MX ? 128 : 64);
-    const TileShape shape = tile_shape(p, a.k_steps, 2, INT_MAX);
+    const TileShape shape = tile_shape(p, a.k_steps, 2, kRun<T>, sizeof(T) == 4 ? 192 : 64);
+    if (a.k_steps > kRun<T> && shape.split == 1) {
+        if constexpr (sizeof(T) == 4) {
+            if (shape.tokens > 128) return launch_one<MX, 192, T, true>(p, a, shape, s);
+            if (shape.tokens > 64) return launch_one<MX, 128, T, true>(p, a, shape, s);
+        }
+        return launch_one<MX, 64, T, true>(p, a, shape, s);
+    }
     if (shape.tokens <= 16) return launch_one<MX, 16, T>(p, a, shape, s);
     if (shape.tokens <= 32) return launch_one<MX, 32, T>(p, a, shape, s);
     if (shape.tokens <= 64) return launch_one<MX, 64, T>(p, a, shape, s);

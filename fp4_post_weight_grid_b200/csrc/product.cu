@@ -75,7 +75,7 @@ TileArgs tile_args(const Product& p, int step_cols, int scale_tile_cols)
     return a;
 }
 
-TileShape tile_shape(const Product& p, int k_steps, int pair, int run)
+TileShape tile_shape(const Product& p, int k_steps, int pair, int run, int most_long)
 {
     const int64_t rows = p.offsets ? (p.m + p.groups - 1) / p.groups : p.m;       // of a group, on average
     const int64_t busy = p.offsets ? std::min<int64_t>(p.groups, p.m) : 1;
@@ -98,7 +98,7 @@ TileShape tile_shape(const Product& p, int k_steps, int pair, int run)
     };
     // Sums longer than a run are put together in shared memory: by one block
     // alone, and in tiles that fit there.
-    const int most = k_steps > run ? 128 : 192;
+    const int most = k_steps > run ? most_long : 192;
     TileShape t{16, 1};
     int64_t best = INT64_MAX;
     for (const int tokens : {16, 32, 64, 128, 160, 192}) {

@@ -28,8 +28,8 @@ struct TileShape {
     int split;       // thread blocks that share a tile's K
 };
 // pair: thread blocks that share a tile of more than 128 tokens; run: steps that
-// one accumulator may sum.
-TileShape tile_shape(const Product& p, int k_steps, int pair, int run);
+// one accumulator may sum; most_long: tokens of a tile whose sums are longer.
+TileShape tile_shape(const Product& p, int k_steps, int pair, int run, int most_long);
 
 // One launch over all tiles: as many clusters of thread blocks (`pair` or the
 // shape's split) as are resident at once, or as there are tiles, if fewer, each

@@ -315,6 +315,49 @@ def test_float_results_of_few_tokens_on_long_columns(fmt, m, n, k):
     assert _norm_off(Problem("linear", fmt, m, n, k, seed=k + n)) <= U * 128 * 2 / 3
 
 
+@pytest.mark.parametrize("fmt", [fq.NVFP4, fq.MXFP4], ids=NAMES.get)
+@pytest.mark.parametrize("m,n,k", [(1, 300, 262144), (16, 19073, 16384), (70, 700, 65536), (300, 2048, 16384),
+                                   (300, 19073, 8192)])
+def test_float_results_of_long_fp4_columns(fmt, m, n, k):
+    # As above; a run is 4096 columns, 64 additions of 64 columns each, and at most 64 runs of a block are added.
+    assert _norm_off(Problem("matmul", fmt, m, n, k, seed=k + n)) <= U * 64 * 2 / 3
+
+
+@pytest.mark.parametrize("fmt", [fq.NVFP4, fq.MXFP4], ids=NAMES.get)
+@pytest.mark.parametrize("m,n,k,counts", [
+    (300, 19073, 4128, None), (170, 19072, 8224, None), (100, 19073, 4128, None), (0, 10001, 4640, [300, 0, 513, 100]),
+    (0, 10000, 4640, [129])])
+def test_exact_long_sums_of_wide_tiles(fmt, m, n, k, counts):
+    # elements 0 and +-1/2, scales up to 4: at most 8224 * 2 * 2 * 4 (mul) in units of 1/16
+    for out in (torch.float32, torch.bfloat16):
+        p = Problem("matmul", fmt, m, n, k, counts=counts, behind=2 if counts else 0, exact=True, bias=True, mul=True, out=out)
+        p.w_codes &= 0x99
+        p.x &= 0x99
+        y, st = p.run()
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        ref, _ = p.reference()
+        inside = ~torch.isnan(ref)
+        assert torch.equal(y[inside], ref[inside].to(out))
+        assert bool((y[~inside] == 77.0).all())
+
+
+@pytest.mark.parametrize("form,fmt", FORMS, ids=form_ids)
+@pytest.mark.parametrize("m,n,counts", [(2, 8, None), (5, 16, None), (0, 16, [3, 0, 2])])
+def test_bf16_results_of_very_long_columns(form, fmt, m, n, counts):
+    # With minus the rounded result as residual an output is a small difference, whose rounding is 2^-9 of at most
+    # 2^-9 of the result.  A run is 65536 columns: 4096 additions of 16 columns for linear, 1024 of 64 for matmul,
+    # with U of the running sum on average each, as above.
+    p = Problem(form, fmt, m, n, 1 << 23, counts=counts, out=torch.bfloat16, seed=n)
+    ref, _ = p.reference()
+    p.residual = (-ref).bfloat16()
+    y, st = p.run()
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    off = y.double() - p.residual.double() - ref
+    assert float(off.norm() / ref.norm()) <= U * (4096 if form == "linear" else 1024) * 2 / 3 + 2.0 ** -17
+
+
 @pytest.mark.parametrize("fmt", [fq.NVFP4, fq.MXFP4], ids=["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("m,k", [(1, 32), (5, 256), (40, 1024), (33, 1056), (200, 544), (300, 4096)])
 def test_token_scales_at_any_word(fmt, m, k):
