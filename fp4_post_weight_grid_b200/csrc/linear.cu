@@ -464,7 +464,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             tc_fence_after();
             if (C::kSplits && a.split > 1) {
                 ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, parity, rank, dead,
-                                         acc_empty + 8 * ac.stage, t + tile_step < tiles, ok);
+                                         acc_empty + 8 * ac.stage, t + tile_step < tiles, ok, nullptr);
             } else {
                 write_tile<T, Chunk<T, BN>::kTokens, C::kEpi>(a, tl, acc, S, part + e * (C::kPart / 4), e, ok);
                 release(ac.stage);
@@ -504,7 +504,7 @@ static cudaError_t launch_one(const Product& p, TileArgs& a, const TileShape& sh
 template <bool MX, typename T> static cudaError_t launch_shape(const Product& p, cudaStream_t s)
 {
     TileArgs a = tile_args(p, kStepCols, MX ? 128 : 64);
-    const TileShape shape = tile_shape(p, a.k_steps, 2, kRun<T>, p.out_bf16 ? 64 : 128);
+    const TileShape shape = tile_shape(p, a.k_steps, 2, {kRun<T>, p.out_bf16 ? 64 : 128, false});
     if (p.out_bf16 && a.k_steps > kRun<T> && shape.split == 1) return launch_one<MX, 64, T, true>(p, a, shape, s);
     if (shape.tokens <= 16) return launch_one<MX, 16, T>(p, a, shape, s);
     if (shape.tokens <= 32) return launch_one<MX, 32, T>(p, a, shape, s);

@@ -33,7 +33,7 @@ constexpr int kMmaCols = 64;
 // its norm after 2048 columns, 9e-7 after 4096, 1.9e-5 after 65536 (a plain
 // binary32 sum of 4096 is off by 4e-7).  So longer float sums come in runs of
 // 4096 columns that are added in shared memory (RUNS), which leaves room for
-// fewer stages: 4096 x 4096 x 14336 NVFP4 takes 143 us so, 128 with the one
+// fewer stages: 4096 x 4096 x 14336 NVFP4 takes 145 us so, 128 with the one
 // accumulator, 140 with the sums in the epilogue's registers.  bf16 ones, whose
 // rounding is 2e-3, come in runs of 65536.
 template <typename T> constexpr int kRun = (sizeof(T) == 4 ? 4096 : 65536) / kStepCols;      // steps
@@ -54,7 +54,7 @@ template <int BN, bool RUNS> struct Config {
     static constexpr int kEpi = BN >= 128 ? 2 : 1;                  // groups of four epilogue warps
     static constexpr int kPart = (kSplits ? BN : RUNS ? BN / kEpi : 32) * kPartRow * 4;      // sums on their way to y, per group
     static constexpr int kThreads = (4 + 4 * kEpi) * 32;
-    static constexpr int kSmem = kStages * kStage + kEpi * kPart + 1024;
+    static constexpr int kSmem = kStages * kStage + (kSplits && RUNS ? 2 : kEpi) * kPart + 1024;
     static constexpr int kResident = 1;
     static_assert(kUsed <= 512 && kCols * kResident <= 512, "tensor memory");
     static_assert(kSmem <= 222 * 1024 && kStage % 1024 == 0, "shared memory");
@@ -318,15 +318,23 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
                 }
             };
             if (RUNS) {
-                float* mine = part + e * (C::kPart / 4);
+                // of a split tile behind its partial sums, which the last run's join
+                const bool split = C::kSplits && a.split > 1;
+                float* mine = part + (split ? 1 : e) * (C::kPart / 4);
                 for (int k = k0; ok && k < k1; k += kRun<T>) {
                     if (k > k0) ac.next();
                     ok = mbar_wait_long(acc_full + 8 * ac.stage, ac.parity, dead);
                     tc_fence_after();
+                    if (split && k + kRun<T> >= k1) break;
                     if (ok) add_to_part<C::kEpi>(tmem + ac.stage * BN, tl.rows, mine, e, k > k0);
                     release(ac.stage);
                 }
-                if (ok) finish_part<T, C::kEpi>(a, tl, S, mine, e);
+                if (split)
+                    ok = write_tile_split<T>(a, tl, tmem + ac.stage * BN, S, part, part_full, part_empty, parity, rank, dead,
+                                             acc_empty + 8 * ac.stage, t + tile_step < tiles, ok,
+                                             k1 - k0 > kRun<T> ? mine : nullptr);
+                else if (ok)
+                    finish_part<T, C::kEpi>(a, tl, S, mine, e);
                 continue;
             }
             const uint32_t acc = tmem + ac.stage * BN;
@@ -334,7 +342,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
             tc_fence_after();
             if (C::kSplits && a.split > 1) {
                 ok = write_tile_split<T>(a, tl, acc, S, part, part_full, part_empty, parity, rank, dead,
-                                         acc_empty + 8 * ac.stage, t + tile_step < tiles, ok);
+                                         acc_empty + 8 * ac.stage, t + tile_step < tiles, ok, nullptr);
             } else {
                 write_tile<T, Chunk<T, BN>::kTokens, C::kEpi>(a, tl, acc, S, part + e * (C::kPart / 4), e, ok);
                 release(ac.stage);
@@ -374,8 +382,8 @@ static cudaError_t launch_one(const Product& p, TileArgs& a, const TileShape& sh
 template <bool MX, typename T> static cudaError_t launch_shape(const Product& p, cudaStream_t s)
 {
     TileArgs a = tile_args(p, kStepCols, MX ? 128 : 64);
-    const TileShape shape = tile_shape(p, a.k_steps, 2, kRun<T>, sizeof(T) == 4 ? 192 : 64);
-    if (a.k_steps > kRun<T> && shape.split == 1) {
+    const TileShape shape = tile_shape(p, a.k_steps, 2, {kRun<T>, sizeof(T) == 4 ? 192 : 64, true});
+    if ((a.k_steps + shape.split - 1) / shape.split > kRun<T>) {
         if constexpr (sizeof(T) == 4) {
             if (shape.tokens > 128) return launch_one<MX, 192, T, true>(p, a, shape, s);
             if (shape.tokens > 64) return launch_one<MX, 128, T, true>(p, a, shape, s);

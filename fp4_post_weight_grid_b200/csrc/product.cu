@@ -75,7 +75,7 @@ TileArgs tile_args(const Product& p, int step_cols, int scale_tile_cols)
     return a;
 }
 
-TileShape tile_shape(const Product& p, int k_steps, int pair, int run, int most_long)
+TileShape tile_shape(const Product& p, int k_steps, int pair, const Runs& runs)
 {
     const int64_t rows = p.offsets ? (p.m + p.groups - 1) / p.groups : p.m;       // of a group, on average
     const int64_t busy = p.offsets ? std::min<int64_t>(p.groups, p.m) : 1;
@@ -96,16 +96,14 @@ TileShape tile_shape(const Product& p, int k_steps, int pair, int run, int most_
         const int64_t slots = tokens > 128 ? sms / pair : sms;
         return (tiles(tokens) * split + slots - 1) / slots * (tokens + 160) / split + (split > 1 ? 40 : 0);
     };
-    // Sums longer than a run are put together in shared memory: by one block
-    // alone, and in tiles that fit there.
-    const int most = k_steps > run ? most_long : 192;
+    const int most = k_steps > runs.steps ? runs.tokens : 192;
     TileShape t{16, 1};
     int64_t best = INT64_MAX;
     for (const int tokens : {16, 32, 64, 128, 160, 192}) {
         if (tokens > most || (tokens >= 32 && tokens / 2 >= rows)) break;
         for (int split = 1; split <= 8; split *= 2) {
             if (split > 1 && (tokens > 64 || split > k_steps || tiles(tokens) * split > sms)) break;
-            if (split > 1 && k_steps > run && (k_steps + split - 1) / split > run) continue;
+            if (split > 1 && !runs.split && (k_steps + split - 1) / split > runs.steps) continue;
             if (cost(tokens, split) <= best) {
                 best = cost(tokens, split);
                 t.tokens = tokens;

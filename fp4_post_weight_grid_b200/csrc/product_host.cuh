@@ -27,9 +27,14 @@ struct TileShape {
     int tokens;      // rows of x per tile, a multiple of 16 (of 32 above 128), at most 192
     int split;       // thread blocks that share a tile's K
 };
-// pair: thread blocks that share a tile of more than 128 tokens; run: steps that
-// one accumulator may sum; most_long: tokens of a tile whose sums are longer.
-TileShape tile_shape(const Product& p, int k_steps, int pair, int run, int most_long);
+// Sums longer than one accumulator may take: its steps, the tokens of a tile that
+// has room for them, and whether blocks that share a tile have.
+struct Runs {
+    int steps, tokens;
+    bool split;
+};
+// pair: thread blocks that share a tile of more than 128 tokens.
+TileShape tile_shape(const Product& p, int k_steps, int pair, const Runs& runs);
 
 // One launch over all tiles: as many clusters of thread blocks (`pair` or the
 // shape's split) as are resident at once, or as there are tiles, if fewer, each

@@ -383,12 +383,14 @@ __device__ __forceinline__ void finish_part(const TileArgs& a, const Tile& t, fl
 // arrive here, `empty` has an arrival from every block that sends here: this
 // tile's have been read (`more`: there is a next one, which waits for that; no
 // signal may reach a block that has ended).
-// `ok`, the warp's: its sums are there.  Returns, to all of the group, whether no
+// `ok`, the warp's: its sums are there; `before`: the sums of the runs before the
+// one in the accumulator, as add_to_part leaves them, or null.  Returns, to all of the group, whether no
 // wait gave up.
 template <typename T, int kSplit>
 __device__ __forceinline__ bool split_tile(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part,
                                            uint32_t full, uint32_t empty, uint32_t parity, uint32_t rank,
-                                           volatile int* dead, uint32_t acc_empty, bool more, bool ok)
+                                           volatile int* dead, uint32_t acc_empty, bool more, bool ok,
+                                           const float* before)
 {
     constexpr int V = kSplit == 8 ? 2 : 4, kEach = 16 / kSplit;      // tokens at a time, of 16 to each block
     using Vec = typename std::conditional<V == 4, uint4, uint2>::type;
@@ -402,6 +404,11 @@ __device__ __forceinline__ bool split_tile(const TileArgs& a, const Tile& t, uin
         for (int c0 = 0; c0 < t.rows; c0 += 16) {
             uint32_t r[16];
             tmem_load16(r, acc + ((uint32_t)quarter << 21) + c0);
+            if (before) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    r[i] = __float_as_uint(before[(c0 + i) * kPartRow + line] + __uint_as_float(r[i]));
+            }
             const uint32_t to = smem_u32(part + ((int)rank * slots + c0 / kSplit) * 128 + line * V);
 #pragma unroll
             for (int d = 0; d < kSplit; ++d)
@@ -464,11 +471,12 @@ __device__ __forceinline__ bool split_tile(const TileArgs& a, const Tile& t, uin
 template <typename T>
 __device__ __forceinline__ bool write_tile_split(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part,
                                                  uint32_t full, uint32_t empty, uint32_t parity, uint32_t rank,
-                                                 volatile int* dead, uint32_t acc_empty, bool more, bool ok)
+                                                 volatile int* dead, uint32_t acc_empty, bool more, bool ok,
+                                                 const float* before)
 {
-    if (a.split == 2) return split_tile<T, 2>(a, t, acc, S, part, full, empty, parity, rank, dead, acc_empty, more, ok);
-    if (a.split == 4) return split_tile<T, 4>(a, t, acc, S, part, full, empty, parity, rank, dead, acc_empty, more, ok);
-    return split_tile<T, 8>(a, t, acc, S, part, full, empty, parity, rank, dead, acc_empty, more, ok);
+    if (a.split == 2) return split_tile<T, 2>(a, t, acc, S, part, full, empty, parity, rank, dead, acc_empty, more, ok, before);
+    if (a.split == 4) return split_tile<T, 4>(a, t, acc, S, part, full, empty, parity, rank, dead, acc_empty, more, ok, before);
+    return split_tile<T, 8>(a, t, acc, S, part, full, empty, parity, rank, dead, acc_empty, more, ok, before);
 }
 
 }  // namespace fp4q

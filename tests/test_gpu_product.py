@@ -326,9 +326,12 @@ def test_float_results_of_long_fp4_columns(fmt, m, n, k):
 @pytest.mark.parametrize("fmt", [fq.NVFP4, fq.MXFP4], ids=NAMES.get)
 @pytest.mark.parametrize("m,n,k,counts", [
     (300, 19073, 4128, None), (170, 19072, 8224, None), (100, 19073, 4128, None), (0, 10001, 4640, [300, 0, 513, 100]),
-    (0, 10000, 4640, [129])])
-def test_exact_long_sums_of_wide_tiles(fmt, m, n, k, counts):
-    # elements 0 and +-1/2, scales up to 4: at most 8224 * 2 * 2 * 4 (mul) in units of 1/16
+    (0, 10000, 4640, [129]),
+    # and of tiles whose columns a cluster splits
+    (128, 4096, 14336, None), (16, 301, 40032, None), (1, 64, 66080, None), (64, 4100, 10272, None),
+    (0, 640, 40032, [5, 0, 300])])
+def test_exact_long_sums_of_wide_and_split_tiles(fmt, m, n, k, counts):
+    # elements 0 and +-1/2, scales up to 4: at most 66080 * 2 * 2 * 4 (mul) = 1.1e6 in units of 1/4
     for out in (torch.float32, torch.bfloat16):
         p = Problem("matmul", fmt, m, n, k, counts=counts, behind=2 if counts else 0, exact=True, bias=True, mul=True, out=out)
         p.w_codes &= 0x99
