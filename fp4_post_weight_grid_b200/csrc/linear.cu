@@ -436,7 +436,7 @@ linear_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         bool ok = true;
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next(), parity ^= 1) {
             const Tile tl = my_tile(t);
-            const float S = MX ? 4.f : a.w_S[tl.group] * 128.f;        // the decoded weights are scaled down
+            const Scale S = scale_of(MX ? 4.f : a.w_S[tl.group] * 128.f);       // the decoded weights are scaled down
             auto release = [&](uint32_t stage) {           // the accumulator has been read by this group
                 tc_fence_before();
                 ok = group_all(e, ok);

@@ -306,7 +306,7 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         bool ok = true;
         for (int64_t t = first_tile; ok && t < tiles; t += tile_step, ac.next(), parity ^= 1) {
             const Tile tl = my_tile(t);
-            const float S = MX ? 1.f : a.w_S[tl.group] * *a.x_S;
+            const Scale S = MX ? scale_of(1.f) : scale_of(a.w_S[tl.group], *a.x_S);
             auto release = [&](uint32_t stage) {           // the accumulator has been read by this group
                 tc_fence_before();
                 ok = group_all(e, ok);

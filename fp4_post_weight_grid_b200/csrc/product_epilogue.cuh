@@ -18,6 +18,20 @@ struct EpilogueArgs {
     int act;
 };
 
+// The factor S of the sums.  The product of two global scales of the quantizers
+// (2^-76 and up each) need not be a normal number; sums then take one after the
+// other, which are.
+struct Scale {
+    float first, second;
+    __device__ __forceinline__ float operator()(float z) const { return z * first * second; }
+};
+__device__ __forceinline__ Scale scale_of(float s) { return {s, 1.f}; }
+__device__ __forceinline__ Scale scale_of(float w, float x)
+{
+    const float s = w * x;
+    return fabsf(s) >= 1.17549435e-38f && fabsf(s) <= 3.40282347e38f ? Scale{s, 1.f} : Scale{w, x};
+}
+
 // Outputs that one thread finishes together: 16 bytes of y.
 template <typename T> struct Lanes {
     static constexpr int kCount = 16 / sizeof(T);

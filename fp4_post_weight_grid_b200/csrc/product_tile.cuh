@@ -214,7 +214,7 @@ template <typename T, int BN> struct Chunk {
 // Columns [c0, c0 + count) of the accumulator; S, bias and act are applied
 // on the way where `last` (the sums are complete).
 template <bool last>
-__device__ __forceinline__ void to_part(uint32_t acc, int c0, int count, float* part, float S, float bias, int act)
+__device__ __forceinline__ void to_part(uint32_t acc, int c0, int count, float* part, const Scale& S, float bias, int act)
 {
     const int quarter = (threadIdx.x / 32) % 4, line = quarter * 32 + (threadIdx.x & 31);
 #pragma unroll 1
@@ -226,7 +226,7 @@ __device__ __forceinline__ void to_part(uint32_t acc, int c0, int count, float* 
         for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(r[i]);
         if (last) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) z[i] = z[i] * S + bias;
+            for (int i = 0; i < 16; ++i) z[i] = S(z[i]) + bias;
             activate(z, act);
         }
 #pragma unroll
@@ -250,7 +250,7 @@ template <typename T> __device__ __forceinline__ float bias_of(const TileArgs& a
 // kGroups-th chunk, through a `part` of its own.  `ok`, the warp's: the sums are
 // there; the group writes where they are for all of its warps.
 template <typename T, int kChunk, int kGroups>
-__device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part, int e,
+__device__ __forceinline__ void write_tile(const TileArgs& a, const Tile& t, uint32_t acc, const Scale& S, float* part, int e,
                                            bool ok)
 {
     constexpr int N = Lanes<T>::kCount, kPer = 128 / N, kItems = kChunk * kPer / 128;
@@ -335,7 +335,7 @@ template <int kGroups> __device__ __forceinline__ void add_to_part(uint32_t acc,
     }
 }
 template <typename T, int kGroups>
-__device__ __forceinline__ void finish_part(const TileArgs& a, const Tile& t, float S, const float* part, int e)
+__device__ __forceinline__ void finish_part(const TileArgs& a, const Tile& t, const Scale& S, const float* part, int e)
 {
     constexpr int N = Lanes<T>::kCount, kPer = 128 / N;
     const int tid = threadIdx.x & 127;
@@ -354,7 +354,7 @@ __device__ __forceinline__ void finish_part(const TileArgs& a, const Tile& t, fl
                 const Extra x = load_extra<T>(a.ep, at);
                 float z[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) z[i] = part[l * kPartRow + lane + i] * S + bias[i];
+                for (int i = 0; i < N; ++i) z[i] = S(part[l * kPartRow + lane + i]) + bias[i];
                 activate(z, a.ep.act);
                 finish<T>(a.ep, z, x, at);
             }
@@ -363,7 +363,7 @@ __device__ __forceinline__ void finish_part(const TileArgs& a, const Tile& t, fl
         const float b = bias_of<T>(a, t, tid);
         for (int c0 = 16 * e, l = 0; c0 < t.rows; c0 += 16 * kGroups, l += 16)
             for (int i = 0; i < 16 && c0 + i < t.rows; ++i) {
-                float z[1] = {part[(l + i) * kPartRow + tid] * S + b};
+                float z[1] = {S(part[(l + i) * kPartRow + tid]) + b};
                 activate(z, a.ep.act);
                 finish_one<T>(a.ep, z[0], (int64_t)(t.row + c0 + i) * a.n + t.feature + tid);
             }
@@ -387,7 +387,7 @@ __device__ __forceinline__ void finish_part(const TileArgs& a, const Tile& t, fl
 // one in the accumulator, as add_to_part leaves them, or null.  Returns, to all of the group, whether no
 // wait gave up.
 template <typename T, int kSplit>
-__device__ __forceinline__ bool split_tile(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part,
+__device__ __forceinline__ bool split_tile(const TileArgs& a, const Tile& t, uint32_t acc, const Scale& S, float* part,
                                            uint32_t full, uint32_t empty, uint32_t parity, uint32_t rank,
                                            volatile int* dead, uint32_t acc_empty, bool more, bool ok,
                                            const float* before)
@@ -456,7 +456,7 @@ __device__ __forceinline__ bool split_tile(const TileArgs& a, const Tile& t, uin
                 }
             }
 #pragma unroll
-            for (int i = 0; i < V; ++i) z[i] = z[i] * S + bias;
+            for (int i = 0; i < V; ++i) z[i] = S(z[i]) + bias;
             activate(z, a.ep.act);
 #pragma unroll
             for (int i = 0; i < V; ++i)
@@ -469,7 +469,7 @@ __device__ __forceinline__ bool split_tile(const TileArgs& a, const Tile& t, uin
     return ok;
 }
 template <typename T>
-__device__ __forceinline__ bool write_tile_split(const TileArgs& a, const Tile& t, uint32_t acc, float S, float* part,
+__device__ __forceinline__ bool write_tile_split(const TileArgs& a, const Tile& t, uint32_t acc, const Scale& S, float* part,
                                                  uint32_t full, uint32_t empty, uint32_t parity, uint32_t rank,
                                                  volatile int* dead, uint32_t acc_empty, bool more, bool ok,
                                                  const float* before)

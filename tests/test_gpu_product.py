@@ -427,6 +427,16 @@ def test_scale_extremes(form, fmt):
     assert torch.equal(y2[:, keep], y[:, keep])
 
 
+@pytest.mark.parametrize("m,n,k,counts", [(3, 200, 96, None), (16, 512, 4096, None), (300, 1000, 4640, None), (0, 130, 96, [2, 0, 40])])
+@pytest.mark.parametrize("w_S,x_S", [(2.0 ** -70, 1.1 * 2.0 ** -70), (1.1 * 2.0 ** -75, 1.3 * 2.0 ** -75), (2.0 ** 52, 1.1 * 2.0 ** 52)])
+def test_global_scales_at_the_ends_of_the_quantizers_range(m, n, k, counts, w_S, x_S):
+    # 2^-64 / 2688 to 2^64 / 2688 each; their product may lie below the normal numbers
+    p = Problem("matmul", fq.NVFP4, m, n, k, counts=counts, behind=1 if counts else 0)
+    p.S.fill_(w_S)
+    p.x_S.fill_(x_S)
+    p.check()
+
+
 @pytest.mark.parametrize("fmt", [fq.NVFP4, fq.MXFP4], ids=NAMES.get)
 @pytest.mark.parametrize("grouped", [False, True])
 def test_non_finite_rows_stay_in_their_rows(fmt, grouped):
