@@ -647,7 +647,8 @@ def fp4q_linear_group(fmt: int, x, offsets, w_codes, w_scales, w_global_scale, y
     """fp4q_linear per group (expert): rows offsets[g] .. offsets[g+1]-1 of x use
     weight g.  `offsets` int32 [groups + 1] on the device, `w_codes` [groups, n,
     k/2], `w_scales` the groups' tiled scales one after the other, bias [groups,
-    n].  Rows outside the offsets are left as they are."""
+    n].  Rows of y outside the offsets are left as they are; such rows of x reach no
+    result but may be read, so nothing may write them during the call."""
     _product("fp4q_linear_group", fmt, x, None, None, offsets, w_codes, w_scales, w_global_scale, y, d_status, bias,
              act, mul, residual, stream)
 

@@ -567,8 +567,11 @@ fp4q_status fp4q_dequant(fp4q_format format, const uint8_t* codes, const uint8_t
  *     with the same sign masks) fp4q_mxfp4_quant_hadamard write it.
  * The group calls multiply the rows of each group (expert) by that group's
  * own weight: rows offsets[g] .. offsets[g+1]-1 of x, mul, residual and y
- * belong to group g, groups may be empty, and rows before offsets[0] or from
- * offsets[groups] on are neither read nor written.
+ * belong to group g, and groups may be empty.  Rows of y, mul and residual
+ * before offsets[0] or from offsets[groups] on are neither written nor read.
+ * Such rows of x (x_codes) reach no result, whatever they hold, but x is copied
+ * in tiles of rows, which may cover them: x must be readable, and must not be
+ * written during the call, over all m rows.
  *
  * Arguments (all four):
  *   fmt         FP4Q_NVFP4 or FP4Q_MXFP4.

@@ -458,6 +458,26 @@ def test_non_finite_rows_stay_in_their_rows(fmt, grouped):
 
 
 @pytest.mark.parametrize("form,fmt", FORMS, ids=form_ids)
+@pytest.mark.parametrize("counts,n,k", [([3, 0, 20], 200, 544), ([300, 1], 10001, 96), ([5, 2], 130, 4128)])
+def test_rows_of_no_group_reach_no_result(form, fmt, counts, n, k):
+    kw = dict(counts=counts, before=3, behind=40, bias=True, mul=True, residual=True, out=torch.bfloat16, act=fq.ACT_SILU)
+    p = Problem(form, fmt, 0, n, k, **kw)
+    want, _ = p.run()
+    p.check(want, torch.zeros(1, dtype=torch.int32, device=DEV))
+    for r in (slice(0, 3), slice(p.m - 40, p.m)):
+        if form == "linear":
+            p.x[r] = torch.nan
+        else:
+            p.x[r] = 0xFF
+            p.x_scales[r] = 0x7F if fmt == fq.NVFP4 else 255
+        p.mul[r] = torch.nan
+        p.residual[r] = torch.inf
+    got, _ = p.run()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("form,fmt", FORMS, ids=form_ids)
 @pytest.mark.parametrize("offsets", [[0, 5, 3, 9], [-1, 2, 3, 9], [0, 2, 3, 10], [0, 2, 2 ** 31 - 1, 9], [9, 0, 0, 0]])
 def test_bad_offsets_are_flagged_and_nothing_is_written(form, fmt, offsets):
     p = Problem(form, fmt, 0, 64, 96, counts=[2, 3, 4])
