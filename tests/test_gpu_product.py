@@ -248,6 +248,31 @@ def test_epilogue(form, fmt, act, out):
 
 
 @pytest.mark.parametrize("form,fmt", FORMS, ids=form_ids)
+@pytest.mark.parametrize("act", [fq.ACT_NONE, fq.ACT_RELU, fq.ACT_GELU, fq.ACT_GELU_TANH, fq.ACT_SILU])
+@pytest.mark.parametrize("m,n", [(5, 130), (37, 136), (300, 19001)])
+def test_activations_of_large_infinite_and_missing_sums(form, fmt, act, m, n):
+    """The bias makes the sums: columns of NaN, both infinities, and magnitudes up to the largest float."""
+    p = Problem(form, fmt, m, n, 64, act=act, exact=True, bias=True)
+    p.x.zero_()
+    z = torch.tensor([torch.nan, torch.inf, -torch.inf, 0.0, 3e38, -3e38, 1e20, -1e20, 1e5, -1e5, 200.0, -200.0, 90.0, -90.0,
+                      20.0, -20.0, 10.5, -10.5, 1e-30, -1e-30], device=DEV)
+    p.bias[0] = z.repeat(n // len(z) + 1)[:n]
+    y, st = p.run()
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    z = p.bias[0]
+    want = _activation(z.double(), act).expand(m, n)
+    if act == fq.ACT_RELU:
+        want = torch.where(torch.isnan(z), z, z.clamp_min(0)).double().expand(m, n)
+    # of -inf, z * Phi(z) and the like are -inf * 0, a NaN, as in 64 bits
+    assert torch.equal(torch.isnan(y), torch.isnan(want))
+    finite = torch.isfinite(want)
+    assert torch.equal(y[torch.isinf(want)].double(), want[torch.isinf(want)])
+    # the functions' bound of _bound; with 3e38 no result may round to infinity
+    assert bool(((y.double() - want).abs()[finite] <= 2.0 ** -20 * (1 + want.abs()[finite])).all())
+
+
+@pytest.mark.parametrize("form,fmt", FORMS, ids=form_ids)
 def test_epilogue_of_groups(form, fmt):
     Problem(form, fmt, 0, 150, 416, counts=[3, 0, 70, 1], before=2, behind=3, act=fq.ACT_SILU, out=torch.bfloat16,
             bias=True, mul=True, residual=True).check()
