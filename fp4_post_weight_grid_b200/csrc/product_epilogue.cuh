@@ -75,7 +75,10 @@ __device__ __forceinline__ uint4 pack16(const float (&v)[8])
 // z * Phi(z) from the rational approximation of erfc by Abramowitz and Stegun,
 // "Handbook of Mathematical Functions", 7.1.26 (absolute error 1.5e-7, a step
 // of binary32 near 1): with x = |z|/sqrt 2, t = 1/(1 + p x), Phi(-|z|) =
-// (a1 t + .. + a5 t^5) exp(-x^2) / 2, so that neither sign of z cancels.
+// (a1 t + .. + a5 t^5) exp(-x^2) / 2, so that neither sign of z cancels.  The
+// result is off by 2.1e-7 at most, by 3e-7 of it for |z| < 1; as the fit's error
+// falls more slowly than the tail, by 5e-5 of it at z = -3 and 1.6e-3 at -5 (about
+// half a step of bf16).
 __device__ __forceinline__ float gelu(float z)
 {
     const float x = fabsf(z) * 0.70710678f, t = __fdividef(1.f, 1.f + 0.3275911f * x);
