@@ -358,10 +358,12 @@ matmul_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__
         cluster_arrive();
         cluster_wait();
     }
-    if (*dead) linger();
     tc_fence_after();
     if (warp == 1) tmem_free<G>(tmem, C::kCols);
-    if (threadIdx.x == 0 && *dead) atomicOr(a.status, FP4Q_FLAG_TIMEOUT);
+    if (*dead) {
+        linger();
+        if (threadIdx.x == 0) atomicOr(a.status, FP4Q_FLAG_TIMEOUT);
+    }
 }
 
 }  // namespace

@@ -3,9 +3,10 @@
 // K, and the way from tensor memory to y.
 //
 // A tile is 128 rows of W (features; 256 where a pair of thread blocks works on
-// it) by up to `tokens` rows of x of one group.  W is the operand that fills the 128 lanes of tensor memory and the
-// tokens are its columns, so that the cost of a tile follows the number of
-// tokens in steps of 16: the same kernel serves one token and thousands.
+// it) by up to `tokens` rows of x of one group.  W is the operand that fills the
+// 128 lanes of tensor memory and the tokens are its columns, so that the cost of a
+// tile follows the number of tokens in steps of 16: the same kernel serves one
+// token and thousands.
 #pragma once
 
 #include <type_traits>
@@ -384,8 +385,8 @@ __device__ __forceinline__ void finish_part(const TileArgs& a, const Tile& t, co
 // tile's have been read (`more`: there is a next one, which waits for that; no
 // signal may reach a block that has ended).
 // `ok`, the warp's: its sums are there; `before`: the sums of the runs before the
-// one in the accumulator, as add_to_part leaves them, or null.  Returns, to all of the group, whether no
-// wait gave up.
+// one in the accumulator, as add_to_part leaves them, or null.  Returns, to all of
+// the group, whether no wait gave up.
 template <typename T, int kSplit>
 __device__ __forceinline__ bool split_tile(const TileArgs& a, const Tile& t, uint32_t acc, const Scale& S, float* part,
                                            uint32_t full, uint32_t empty, uint32_t parity, uint32_t rank,

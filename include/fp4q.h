@@ -602,11 +602,12 @@ fp4q_status fp4q_dequant(fp4q_format format, const uint8_t* codes, const uint8_t
  * them; a NaN pattern makes the outputs that it reaches NaN.
  * The results of a call do not depend on other work or on the run: sums are
  * taken in a fixed order.
- * The tensor cores truncate where they add.  Float results are therefore summed
- * in runs (2048 columns, fp4q_matmul 4096) that are added with rounding: the norm
- * of the error stays below 1.4e-6 of the result's (fp4q_matmul 1.1e-6), however
- * large k is.  For bf16 results, which are rounded by 2^-9 anyway, a run is 65536
- * columns, within 2.7e-5.
+ * The tensor cores truncate where they add, 16 columns at a time (fp4q_matmul 64).
+ * Float results are therefore summed in runs (2048 columns, fp4q_matmul 4096) that
+ * are added with rounding: on terms of random signs the norm of the error is 1.3e-6
+ * of the result's (fp4q_matmul 1.0e-6), however large k is; it is at most one step
+ * of binary32 per addition of a run, of its own sum.  For bf16 results, which are
+ * rounded by 2^-9 anyway, a run is 65536 columns (2.7e-5).
  * Errors: FP4Q_ERR_DTYPE (fmt, out_dt), FP4Q_ERR_SHAPE (negative sizes, k not
  * a positive multiple of 32 or above 2^26, m or groups * n above 2^31 - 1 - 256,
  * a tensor that overflows), FP4Q_ERR_ARG (act, too many groups), FP4Q_ERR_NULL,
