@@ -341,6 +341,13 @@ def test_float_results_of_few_tokens_on_long_columns(fmt, m, n, k):
 
 
 @pytest.mark.parametrize("fmt", [fq.NVFP4, fq.MXFP4], ids=NAMES.get)
+@pytest.mark.parametrize("m,n,k", [(16, 300, 262144), (40, 700, 65536), (120, 10001, 32768), (300, 2048, 65536)])
+def test_float_results_of_more_tokens_on_long_columns(fmt, m, n, k):
+    # As above, in runs of 2048 columns; one accumulator would be off by 6e-6 to 2.6e-5.
+    assert _norm_off(Problem("linear", fmt, m, n, k, seed=k + n)) <= U * 128 * 2 / 3
+
+
+@pytest.mark.parametrize("fmt", [fq.NVFP4, fq.MXFP4], ids=NAMES.get)
 @pytest.mark.parametrize("m,n,k", [(1, 300, 262144), (16, 19073, 16384), (70, 700, 65536), (300, 2048, 16384),
                                    (300, 19073, 8192)])
 def test_float_results_of_long_fp4_columns(fmt, m, n, k):
